@@ -211,8 +211,8 @@ def prepare(case, seed):
         st["out"] = torch.empty((n, h, d), dtype=dt, device=dev)
         # the length bound that a scheduler knows, and a workspace for it, kept from call to call
         st["max_len"] = max(lens)
-        st["ws"] = pi.alloc_attend_workspace(st["cache"], h, n, case["new"], max_len=st["max_len"],
-                                             score=case["score"])
+        st["ws"] = pi.alloc_attend_workspace(st["cache"], h, case["new"], max_len=st["max_len"],
+                                             add_score=case["score"])
         st["attend"] = pi.attend
     return st
 
