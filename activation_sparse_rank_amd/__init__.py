@@ -29,4 +29,15 @@ from .api import (  # noqa: F401
     sparse_ffn,
     workspace_bytes,
 )
+from .attention import (  # noqa: F401
+    KVCache,
+    Rope,
+    alloc_attend_workspace,
+    attend,
+    attend_workspace_bytes,
+    kv_append,
+    kv_evict,
+    kv_read,
+    qk_rope,
+)
 from ._lib import load as load_library  # noqa: F401

@@ -14,6 +14,9 @@ LIB_PATH = os.path.join(_HERE, "libpi.so")
 PI_OK, PI_E_NULL, PI_E_SHAPE, PI_E_DTYPE, PI_E_ALIGN, PI_E_RANGE, PI_E_WORKSPACE, PI_E_HIP = range(8)
 PI_F32, PI_F16, PI_Q4_0 = 0, 1, 2
 PI_RELU, PI_REGLU, PI_RELU2 = 0, 1, 2
+PI_ROPE_HALF, PI_ROPE_INTERLEAVED = 0, 1
+PI_KV_BLOCK = 32              # tokens of a cache block (pi.h)
+PI_KV_EVICT_IN_PLACE = 16384  # most blocks of a table row that pi_kv_evict works on in place (pi.h)
 
 STATUS_NAMES = {
     PI_OK: "PI_OK", PI_E_NULL: "PI_E_NULL", PI_E_SHAPE: "PI_E_SHAPE", PI_E_DTYPE: "PI_E_DTYPE",
@@ -23,7 +26,8 @@ STATUS_NAMES = {
 # Every symbol include/pi.h declares.
 EXPORTS = ("pi_workspace_bytes", "pi_clear_flags", "pi_read_flags", "pi_read_down_rows", "pi_read_up_rows", "pi_predict", "pi_compact",
            "pi_sparse_ffn", "pi_layer", "pi_layer_noalloc", "pi_q4_0_repack", "pi_count_active", "pi_hot_order",
-           "pi_rank_order", "pi_permute_rows", "pi_stream_read", "pi_gather_read", "pi_status_str", "pi_last_error")
+           "pi_rank_order", "pi_permute_rows", "pi_stream_read", "pi_gather_read", "pi_status_str", "pi_last_error",
+           "pi_qk_rope", "pi_kv_append", "pi_kv_read", "pi_attend_workspace_bytes", "pi_attend", "pi_kv_evict")
 
 PI_SEGMENT_ROWS = 32   # neurons per segment of pi_layer's fused kernel (pi.h)
 PI_STREAM_BLOCKS = 2048  # entries of pi_stream_read's output (pi.h)
@@ -33,7 +37,7 @@ PI_WS_HEADER_BYTES = 256
 PI_WS_FLAGS, PI_WS_WAIT_POLLS, PI_WS_SKIP_PUBLISH = 0, 1, 2
 PI_WS_DOWN_ROWS = 4   # 64-bit count of down-projection rows read, words 4 and 5
 PI_WS_UP_ROWS = 6     # 64-bit count of w_up rows read, words 6 and 7
-PI_FLAG_WAIT_EXPIRED, PI_FLAG_FP16_RANGE = 1, 2
+PI_FLAG_WAIT_EXPIRED, PI_FLAG_FP16_RANGE, PI_FLAG_KV_RANGE = 1, 2, 4
 PI_NOALLOC_SCRATCH_BYTES = 32 << 20   # static scratch of pi_layer_noalloc (pi.h)
 
 
@@ -47,6 +51,19 @@ class PiFFN(ctypes.Structure):
     _fields_ = [("d_model", ctypes.c_int32), ("d_ff", ctypes.c_int32), ("act", ctypes.c_int32),
                 ("wtype", ctypes.c_int32), ("w_up", ctypes.c_void_p), ("w_gate", ctypes.c_void_p),
                 ("w_down_t", ctypes.c_void_p), ("b_up", ctypes.c_void_p), ("b_gate", ctypes.c_void_p)]
+
+
+class PiRope(ctypes.Structure):
+    _fields_ = [("head_dim", ctypes.c_int32), ("rot", ctypes.c_int32), ("layout", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("eps", ctypes.c_float), ("freqs", ctypes.c_void_p),
+                ("q_norm", ctypes.c_void_p), ("k_norm", ctypes.c_void_p)]
+
+
+class PiKVCache(ctypes.Structure):
+    _fields_ = [("n_seqs", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("max_blocks", ctypes.c_int32), ("n_pages", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("pages", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("open", ctypes.c_void_p),
+                ("table", ctypes.c_void_p), ("score", ctypes.c_void_p)]
 
 
 _lib = None
@@ -98,6 +115,19 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.pi_stream_read.restype = ctypes.c_int
     lib.pi_gather_read.argtypes = [P, i32, i32, P, P, i32, P, P]
     lib.pi_gather_read.restype = ctypes.c_int
+    i64 = ctypes.c_int64
+    lib.pi_qk_rope.argtypes = [PP(PiRope), P, i64, i64, i32, P, i64, i64, i32, P, i32, i32, P, i64, i64, P, i64, i64, P]
+    lib.pi_qk_rope.restype = ctypes.c_int
+    lib.pi_kv_append.argtypes = [PP(PiKVCache), P, i64, i64, P, i64, i64, i32, P, P, i32, P]
+    lib.pi_kv_append.restype = ctypes.c_int
+    lib.pi_kv_read.argtypes = [PP(PiKVCache), P, P, i32, P, i64, i64, P, i64, i64, i32, P]
+    lib.pi_kv_read.restype = ctypes.c_int
+    lib.pi_attend_workspace_bytes.argtypes = [PP(PiKVCache), i32, i32, i32, i32]
+    lib.pi_attend_workspace_bytes.restype = sz
+    lib.pi_attend.argtypes = [PP(PiKVCache), P, i64, i64, i32, i32, P, P, i32, i32, f32, i32, P, i64, i64, P, sz, P]
+    lib.pi_attend.restype = ctypes.c_int
+    lib.pi_kv_evict.argtypes = [P, P, P, i32, i32, i32, i32, i32, P, P, P, P]
+    lib.pi_kv_evict.restype = ctypes.c_int
     lib.pi_status_str.argtypes = [ctypes.c_int]
     lib.pi_status_str.restype = ctypes.c_char_p
     lib.pi_last_error.argtypes = []

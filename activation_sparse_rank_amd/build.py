@@ -23,7 +23,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libpi.so")
 
-SOURCES = ["abi.hip", "k_predict.hip", "k_compact.hip", "k_gather.hip", "k_mfma.hip", "k_q4.hip", "k_place.hip", "k_stream.hip"]
+SOURCES = ["abi.hip", "k_predict.hip", "k_compact.hip", "k_gather.hip", "k_mfma.hip", "k_q4.hip", "k_place.hip", "k_stream.hip",
+           "abi_attn.hip", "k_rope.hip", "k_kvcache.hip", "k_attend.hip", "k_evict.hip"]
 
 ARCH = "gfx950"
 CFLAGS = [

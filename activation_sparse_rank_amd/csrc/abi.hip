@@ -273,6 +273,8 @@ hipError_t static_scratch(hipStream_t s, char** out) {
 
 }  // namespace
 
+pi_status pi::hip_failed(hipError_t e) { return hip_fail(e); }
+
 extern "C" {
 
 size_t pi_workspace_bytes(const pi_predictor* pred, const pi_ffn* ffn, int32_t n_tok) {
