@@ -9,8 +9,8 @@
 // vs / vref out again once per block.  O^T += V^T P^T with P in fp16.  A lane holds
 // the weights of 8 tokens of one row, which is what the second product's
 // operand takes from it: P never leaves the registers.  The reference
-// exponent m moves only when a logit passes it by 2^8 (a ballot sees it), so
-// the sums are seldom rescaled; 2^8 fits fp16 by far.
+// exponent m moves only when the weights of a block outgrow fp16's range above it (a
+// ballot sees their sum), so maxima are seldom taken and sums seldom rescaled.
 //
 // The pages' byte order gives each lane its 16 codes of an operand in one
 // 16-byte load, 1 KB in a row for a wave.
@@ -27,20 +27,23 @@ namespace {
 
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
+typedef float f32x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kAtThreads = 256;
 constexpr int kAtWaves = kAtThreads / kWave;
 constexpr int kMaxSplits = 64;
-constexpr float kSlack = 8.f;        // log2 of what a weight may pass the reference by
 constexpr float kNoMax = -1e30f;     // reference before the first visible token
-// Weights are held times 2^6: with the slack and a value scale's ratio below
-// 2 they stay under 2^15, and what a weight loses below fp16's smallest step
-// is at most 2^-31 of the row's largest weight, so that 10^5 such tokens
-// beside one that takes the row are still counted.
+// Weights are held times 2^6, and a lane's eight of a block may sum to 2^15
+// (fp16 holds 65504) before the reference moves: no maximum is taken but
+// then.  What a weight loses below fp16's smallest step is at most 2^-31 of the
+// row's largest weight, so that 10^5 such tokens beside one that takes the
+// row are still counted.
 constexpr float kBias = 6.f;
-// Blocks with value scales under this share of the wave's largest take a
-// product of their own, scaled in fp32: their weights would leave fp16's range.
-constexpr float kSmall = 0x1p-10f;
+constexpr float kMost = 0x1p15f;
+// Under this share of the wave's largest value scale a block's weights would
+// leave fp16's range: the sums are brought to the block's scale (a power of
+// two, exact, 2^-60 at least) for its product and back.
+constexpr float kSmall = 0x1p-10f, kSmallest = 0x1p-60f;
 
 __device__ __forceinline__ f32x4 mfma16(f16x8 a, f16x8 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
@@ -91,12 +94,18 @@ __device__ void nan_rows(const AttendArgs& a, const Seq& q, int h, int d, int64_
   }
 }
 
+// Waves that a SIMD holds: what the registers of a wave's rows leave.
+constexpr int waves_per_simd(int d, int nb, bool f32) {
+  return d * nb * (f32 ? 2 : 1) <= 64 ? 4 : (d * nb * (f32 ? 2 : 1) <= 128 ? 3 : 2);
+}
+
 // T: rows (fp16; fp32 as two fp16 parts).  NB: 16-row tiles of a wave.
 // SCORE: the weights of each block are wanted.  ROWS: see above.
 template <typename T, int D, int NB, bool SCORE, bool ROWS>
-__global__ __launch_bounds__(kAtThreads) void k_attend(AttendArgs a) {
+__global__ __launch_bounds__(kAtThreads, waves_per_simd(D, NB, sizeof(T) == 4)) void k_attend(AttendArgs a) {
   constexpr int KK = D / 64, DT = D / 16, DB = D / 32;
-  constexpr bool kTwo = sizeof(T) == 4;             // two fp16 parts of q and p
+  constexpr bool kTwo = sizeof(T) == 4;             // two fp16 parts of q
+  constexpr bool kTwoP = kTwo || !ROWS;             // and of p: always where the pages' bytes bound the time
   const int pairs = a.n_seqs * a.hk;
   const int pair = blockIdx.x % pairs;
   const int tile = blockIdx.x / pairs % a.tiles;
@@ -184,21 +193,39 @@ __global__ __launch_bounds__(kAtThreads) void k_attend(AttendArgs a) {
   }
   float vref = 0x1p-126f;                           // o is in units of it
 
-  struct Raw { u32x4 k[2 * KK], v[DB]; };
+  u32x4 rk[2 * KK], rv[DB];                         // a block's codes, as they lie in the page
   bool bad = false;
   for (int base = 0; base < mine; base += kWave) {
     const int cnt = mine - base < kWave ? mine - base : kWave;
     // Lane i: page and scales of the i-th block.
     int page = 0;
     float ks = 0.f, vs = 0.f;
+    bool no_page = false;
     if (lane < cnt) {
       page = a.table[(int64_t)pair * a.max_blocks + start + (base + lane) * kStep];
-      if ((unsigned)page < (unsigned)a.n_pages) {
-        const float2 sc = reinterpret_cast<const float2*>(a.scales)[page];
-        ks = sc.x, vs = sc.y;
-      } else {
-        page = 0, ks = -1.f, bad = true;
-      }
+      no_page = (unsigned)page >= (unsigned)a.n_pages;
+      page = no_page ? 0 : page;
+      bad |= no_page;
+    }
+    auto page_at = [&](int i) {
+      return a.pages + (int64_t)__builtin_amdgcn_readlane(page, i) * (2 * kBlk * D) + lane * 16;
+    };
+    auto load_k = [&](int i) {
+      const uint8_t* p = page_at(i);
+#pragma unroll
+      for (int u = 0; u < 2 * KK; ++u) rk[u] = ROWS ? ld16(p + u * 1024) : ld_nt(p + u * 1024);
+    };
+    auto load_v = [&](int i) {
+      const uint8_t* p = page_at(i) + kBlk * D;
+#pragma unroll
+      for (int u = 0; u < DB; ++u) rv[u] = ROWS ? ld16(p + u * 1024) : ld_nt(p + u * 1024);
+    };
+    // The first block's codes are on their way while the scales come.
+    load_k(0);
+    load_v(0);
+    if (lane < cnt) {
+      const float2 sc = reinterpret_cast<const float2*>(a.scales)[page];
+      ks = no_page ? -1.f : sc.x, vs = sc.y;
       // A scale that is no number: what sees the block is NaN, through its logits.
       if (!(ks >= 0.f && ks < __builtin_inff() && vs >= 0.f && vs < __builtin_inff())) ks = quiet_nan(), vs = 0.f;
     }
@@ -215,119 +242,120 @@ __global__ __launch_bounds__(kAtThreads) void k_attend(AttendArgs a) {
       vref = vtop;
     }
     const float ratio = vs > 0.f ? vs / vref : 1.f;
-    const bool small = ratio < kSmall;
-    const float lr = (small ? 0.f : log2_hw(ratio)) + kBias, iv = small ? 1.f : 1.f / ratio;
-    const unsigned long long smalls = __ballot(small);
+    const unsigned long long smalls = __ballot(ratio < kSmall);
+    const float unit = ratio < kSmall ? as_f(__builtin_bit_cast(unsigned, fmaxf(ratio, kSmallest)) & 0x7f800000u) : 1.f;
+    const float share = fmaxf(ratio / unit, 0x1p-60f);
+    const float lr = log2_hw(share) + kBias, iv = 1.f / share;
 
-    auto load = [&](int i, Raw& r) {
-      const int pg = __builtin_amdgcn_readlane(page, i);
-      const uint8_t* p = a.pages + (int64_t)pg * (2 * kBlk * D) + lane * 16;
-#pragma unroll
-      for (int u = 0; u < 2 * KK; ++u) r.k[u] = ROWS ? ld16(p + u * 1024) : ld_nt(p + u * 1024);
-#pragma unroll
-      for (int u = 0; u < DB; ++u) r.v[u] = ROWS ? ld16(p + kBlk * D + u * 1024) : ld_nt(p + kBlk * D + u * 1024);
-    };
-    auto block = [&](int i, const Raw& r) {
+    // One set of registers for the codes: the next block's keys are on their
+    // way from the end of the first product on, its values from the second's.
+    for (int i = 0; i < cnt; ++i) {
       const int b = start + (base + i) * kStep;
-      const float ksc = lane_f(ks, i) * a.scale, lrb = lane_f(lr, i), ivb = lane_f(iv, i);
-      f16x8 kf[2][KK][2];
+      const float ksc = lane_f(ks, i) * a.scale;
+      const float lrb = lane_f(lr, i), ivb = lane_f(iv, i);
+      f32x4 st[NB][2];
 #pragma unroll
-      for (int u = 0; u < 2 * KK; ++u) {
-        kf[u / KK][u % KK][0] = codes_f16(r.k[u].x, r.k[u].y);
-        kf[u / KK][u % KK][1] = codes_f16(r.k[u].z, r.k[u].w);
-      }
-      const bool edge = (b + 1) * kBlk > kmin;      // some row does not see all of the block
-      f16x8 pf[NB], pl[NB];
+      for (int nb = 0; nb < NB; ++nb) st[nb][0] = st[nb][1] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb) {
-        f32x4 st[2];
+      for (int kk = 0; kk < KK; ++kk)
 #pragma unroll
-        for (int mb = 0; mb < 2; ++mb) {
-          st[mb] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int f = 0; f < 2; ++f)
 #pragma unroll
-          for (int kk = 0; kk < KK; ++kk)
+          for (int mb = 0; mb < 2; ++mb) {
+            const u32x4 w = rk[mb * KK + kk];
+            const f16x8 kf = f ? codes_f16(w.z, w.w) : codes_f16(w.x, w.y);
 #pragma unroll
-            for (int f = 0; f < 2; ++f) {
-              st[mb] = mfma16(kf[mb][kk][f], qf[nb][kk][f], st[mb]);
-              if constexpr (kTwo) st[mb] = mfma16(kf[mb][kk][f], ql[nb][kk][f], st[mb]);
+            for (int nb = 0; nb < NB; ++nb) {
+              st[nb][mb] = mfma16(kf, qf[nb][kk][f], st[nb][mb]);
+              if constexpr (kTwo) st[nb][mb] = mfma16(kf, ql[nb][kk][f], st[nb][mb]);
             }
-        }
-        float sc = kTwo ? ksc * rs[nb] : ksc;
-        if (edge) {
+          }
+      if (i + 1 < cnt) load_k(i + 1);
+      const bool edge = (b + 1) * kBlk > kmin;      // some row does not see all of the block
+      auto scale_of = [&](int nb) { return kTwo ? ksc * rs[nb] : ksc; };
+      if (edge) {
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          const float sc = scale_of(nb);
 #pragma unroll
           for (int mb = 0; mb < 2; ++mb)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-              st[mb][j] = b * kBlk + mb * 16 + 4 * g + j < sees[nb] ? st[mb][j] * sc : -__builtin_inff();
-          sc = 1.f;
+              st[nb][mb][j] = b * kBlk + mb * 16 + 4 * g + j < sees[nb] ? st[nb][mb][j] * sc : -__builtin_inff();
         }
-        float top = fmaxf(fmaxf(fmaxf(st[0][0], st[0][1]), fmaxf(st[0][2], st[0][3])),
-                          fmaxf(fmaxf(st[1][0], st[1][1]), fmaxf(st[1][2], st[1][3]))) * sc;
-        if (__any(top > m[nb] + kSlack)) {
+      }
+      f16x8 pf[NB], pl[NB];
+      float sum[NB];
+      auto weights = [&](int nb) {
+        const float sc = edge ? 1.f : scale_of(nb), off = lrb - m[nb];
+        float p[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) p[j] = exp2_hw(__builtin_fmaf(st[nb][j / 4][j % 4], sc, off));
+        const f32x8 pv = {p[0], p[1], p[2], p[3], p[4], p[5], p[6], p[7]};
+        pf[nb] = __builtin_convertvector(pv, f16x8);
+        if constexpr (kTwoP) pl[nb] = __builtin_convertvector(pv - __builtin_convertvector(pf[nb], f32x8), f16x8);
+        if constexpr (kTwoP || SCORE) {
+          sum[nb] = (p[0] + p[1] + (p[2] + p[3])) + (p[4] + p[5] + (p[6] + p[7]));
+        } else {
+          // the sum of the rounded weights, which the second product multiplies
+          const u32x4 w = __builtin_bit_cast(u32x4, pf[nb]);
+          const f16x2 one = {(f16)1.f, (f16)1.f};
+          float x = __builtin_amdgcn_fdot2(as_h2(w.x), one, 0.f, false);
+          x = __builtin_amdgcn_fdot2(as_h2(w.y), one, x, false);
+          x = __builtin_amdgcn_fdot2(as_h2(w.z), one, x, false);
+          sum[nb] = __builtin_amdgcn_fdot2(as_h2(w.w), one, x, false);
+        }
+      };
+      bool over = false;
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        weights(nb);
+        over |= !(sum[nb] < kMost);
+      }
+      if (__any(over)) {                            // a weight passes the reference by too much: move it
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          const f32x4 s0 = st[nb][0], s1 = st[nb][1];
+          const float top = fmaxf(fmaxf(fmaxf(s0[0], s0[1]), fmaxf(s0[2], s0[3])),
+                                  fmaxf(fmaxf(s1[0], s1[1]), fmaxf(s1[2], s1[3]))) * (edge ? 1.f : scale_of(nb));
           const float mn = fmaxf(m[nb], row_max(top));
           const float f = exp2_hw(m[nb] - mn);
           m[nb] = mn;
           l[nb] *= f;
 #pragma unroll
           for (int t = 0; t < DT; ++t) o[nb][t] *= f;
+          weights(nb);
         }
-        const float off = lrb - m[nb];
-        float p[8];
+      }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) p[j] = exp2_hw(__builtin_fmaf(st[j / 4][j % 4], sc, off));
-        const float sum = (p[0] + p[1] + (p[2] + p[3])) + (p[4] + p[5] + (p[6] + p[7]));
-        l[nb] = __builtin_fmaf(sum, ivb, l[nb]);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          pf[nb][j] = (f16)p[j];
-          if constexpr (kTwo) pl[nb][j] = (f16)(p[j] - (float)pf[nb][j]);
-        }
+      for (int nb = 0; nb < NB; ++nb) {
+        l[nb] = __builtin_fmaf(sum[nb], ivb, l[nb]);
         if constexpr (SCORE) {
-          const float w = row_sum(sum) * ivb;
+          const float w = row_sum(sum[nb]) * ivb;
           const int r = r0 + nb * 16 + c;
           if (g == 0 && r < rows) a.lse[((int64_t)pair * a.max_nb + b) * a.r_max + r] = m[nb] + log2_hw(w);
         }
       }
-      if (smalls >> i & 1) {
-        const float rb = lane_f(ratio, i);
-        const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+      auto rescale = [&](float f) {
 #pragma unroll
-        for (int t = 0; t < DT; ++t) {
-          const u32x4 w = r.v[t / 2];
-          const f16x8 v = t % 2 ? codes_f16(w.z, w.w) : codes_f16(w.x, w.y);
+        for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-          for (int nb = 0; nb < NB; ++nb) {
-            f32x4 x = mfma16(v, pf[nb], zero);
-            if constexpr (kTwo) x = mfma16(v, pl[nb], x);
-            o[nb][t] += x * rb;
-          }
-        }
-        return;
-      }
+          for (int t = 0; t < DT; ++t) o[nb][t] *= f;
+      };
+      const bool far = smalls >> i & 1;
+      if (far) rescale(1.f / lane_f(unit, i));
 #pragma unroll
-      for (int u = 0; u < DB; ++u) {
-        const f16x8 v0 = codes_f16(r.v[u].x, r.v[u].y), v1 = codes_f16(r.v[u].z, r.v[u].w);
+      for (int t = 0; t < DT; ++t) {
+        const u32x4 w = rv[t / 2];
+        const f16x8 v = t % 2 ? codes_f16(w.z, w.w) : codes_f16(w.x, w.y);
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
-          o[nb][2 * u] = mfma16(v0, pf[nb], o[nb][2 * u]);
-          o[nb][2 * u + 1] = mfma16(v1, pf[nb], o[nb][2 * u + 1]);
-          if constexpr (kTwo) {
-            o[nb][2 * u] = mfma16(v0, pl[nb], o[nb][2 * u]);
-            o[nb][2 * u + 1] = mfma16(v1, pl[nb], o[nb][2 * u + 1]);
-          }
+          o[nb][t] = mfma16(v, pf[nb], o[nb][t]);
+          if constexpr (kTwoP) o[nb][t] = mfma16(v, pl[nb], o[nb][t]);
         }
       }
-    };
-    // Two register stages: the next block's codes are in flight.
-    Raw ra, rb;
-    load(0, ra);
-    for (int i = 0; i < cnt; i += 2) {
-      if (i + 1 < cnt) load(i + 1, rb);
-      block(i, ra);
-      if (i + 1 < cnt) {
-        if (i + 2 < cnt) load(i + 2, ra);
-        block(i + 1, rb);
-      }
+      if (far) rescale(lane_f(unit, i));
+      if (i + 1 < cnt) load_v(i + 1);
     }
   }
   raise_flag_if_any(a.flags, bad, PI_FLAG_KV_RANGE);
@@ -526,9 +554,9 @@ AttendPlan attend_plan(int n_seqs, int hk, int group, int d, int dtype, int max_
   const int cap = max_tiles(d, dtype == PI_F32);
   p.nb = 1;
   while (p.nb < cap && p.nb * 16 < p.r_max) p.nb *= 2;
-  // Waves with rows of their own where that fills the CUs.
+  // Waves with rows of their own where that fills the waves and the CUs.
   const int own = (p.r_max + 16 * cap * kAtWaves - 1) / (16 * cap * kAtWaves);
-  p.rows = pairs * own >= 256;
+  p.rows = p.r_max >= 16 * cap * kAtWaves && pairs * own >= 256;
   p.tiles = p.rows ? own : (p.r_max + 16 * p.nb - 1) / (16 * p.nb);
   int64_t splits = 1;
   if (!p.rows) {
