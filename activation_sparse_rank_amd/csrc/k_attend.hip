@@ -119,7 +119,7 @@ __global__ __launch_bounds__(kAtThreads, waves_per_simd(D, NB, sizeof(T) == 4)) 
     return;
   }
   const int rows = q.n * a.group;
-  const int r0 = (ROWS ? tile * kAtWaves + wave : tile) * 16 * NB;
+  const int r0 = tile * 16 * NB;
   if (r0 >= rows) return;
   const int seen0 = q.len - q.n + 1;                // tokens that the sequence's first row sees (may be < 1)
   const int r1 = r0 + 16 * NB < rows ? r0 + 16 * NB : rows;
@@ -128,8 +128,8 @@ __global__ __launch_bounds__(kAtThreads, waves_per_simd(D, NB, sizeof(T) == 4)) 
   const int nbk = (kmax + kBlk - 1) / kBlk;
   const int per = (nbk + a.splits - 1) / a.splits;
   const int b0 = split * per, b1 = b0 + per < nbk ? b0 + per : nbk;
-  constexpr int kStep = ROWS ? 1 : kAtWaves;
-  const int start = b0 + (ROWS ? 0 : wave);
+  constexpr int kStep = kAtWaves;
+  const int start = b0 + wave;
   const int mine = start < b1 ? (b1 - start + kStep - 1) / kStep : 0;
 
   // Queries: lane (g, c) has elements 64 kk + 16 g .. + 16 of row c.
@@ -369,22 +369,7 @@ __global__ __launch_bounds__(kAtThreads, waves_per_simd(D, NB, sizeof(T) == 4)) 
   auto out_row = [&](int r) {
     return static_cast<T*>(a.out) + (int64_t)(q.q0 + r / a.group) * a.o_ts + (int64_t)(h * a.group + r % a.group) * a.o_hs;
   };
-  if constexpr (ROWS) {
-#pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-      const int r = r0 + nb * 16 + c;
-      if (r >= rows) continue;
-      T* p = out_row(r);
-      const float inv = l[nb] == 0.f ? 0.f : 1.f / l[nb];
-#pragma unroll
-      for (int t = 0; t < DT; ++t) {
-        const f32x4 v = o[nb][t] * inv;
-        if constexpr (kTwo) *reinterpret_cast<f32x4*>(p + 16 * t + 4 * g) = v;
-        else *reinterpret_cast<f16x4*>(p + 16 * t + 4 * g) = __builtin_convertvector(v, f16x4);
-      }
-      if (SCORE && g == 0) a.ml[(int64_t)pair * a.r_max + r] = float2{m[nb], l[nb]};
-    }
-  } else {
+  {
     // The four waves' sums, added in wave order.
     __shared__ float so[kAtWaves][16][D + 4];
     __shared__ float sm[kAtWaves][16], sl[kAtWaves][16];
@@ -460,21 +445,28 @@ __global__ __launch_bounds__(kAtThreads) void k_attend_join(AttendArgs a, int ro
     const int pair = blockIdx.x / a.r_max, r = blockIdx.x % a.r_max;
     const Seq q = read_seq(a.lens, a.q_start, pair / a.hk, a.max_q, a.n_tok, a.max_len);
     if (!q.ok || r >= q.n * a.group) return;
-    const int lane = lane_id();
+    // Every split's part of this thread's elements, in flight while the weights are found.
+    const int lane = lane_id(), part = threadIdx.x / L, e = threadIdx.x % L * 4;
+    constexpr int N = kMaxSplits / G;
+    f32x4 x[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const int i = k * G + part < a.splits ? k * G + part : 0;
+      x[k] = *reinterpret_cast<const f32x4*>(a.part + (((int64_t)i * pairs + pair) * a.r_max + r) * D + e);
+    }
     float2 v = {kNoMax, 0.f};
     if (lane < a.splits) v = a.ml[((int64_t)lane * pairs + pair) * a.r_max + r];
     float top = v.x;
 #pragma unroll
-    for (int x = 32; x >= 1; x >>= 1) top = fmaxf(top, __shfl_xor(top, x, kWave));
+    for (int y = 32; y >= 1; y >>= 1) top = fmaxf(top, __shfl_xor(top, y, kWave));
     const float f = exp2_hw(v.x - top);
     const float sum = wave_sum(f * v.y);
-    const int part = threadIdx.x / L, e = threadIdx.x % L * 4;
     f32x4 o = {0.f, 0.f, 0.f, 0.f};
-    for (int i0 = 0; i0 < a.splits; i0 += G) {
-      const int i = i0 + part;
-      const float w = __shfl(f, i & 63, kWave);
-      if (i < a.splits)
-        o += w * *reinterpret_cast<const f32x4*>(a.part + (((int64_t)i * pairs + pair) * a.r_max + r) * D + e);
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const int i = k * G + part;
+      const float w = __shfl(f, i, kWave);
+      o += i < a.splits ? w * x[k] : f32x4{0.f, 0.f, 0.f, 0.f};
     }
     acc[part][e / 4] = o;
     __syncthreads();
@@ -555,7 +547,7 @@ AttendPlan attend_plan(int n_seqs, int hk, int group, int d, int dtype, int max_
   p.nb = 1;
   while (p.nb < cap && p.nb * 16 < p.r_max) p.nb *= 2;
   // Waves with rows of their own where that fills the waves and the CUs.
-  const int own = (p.r_max + 16 * cap * kAtWaves - 1) / (16 * cap * kAtWaves);
+  const int own = (p.r_max + 16 * cap - 1) / (16 * cap);
   p.rows = p.r_max >= 16 * cap * kAtWaves && pairs * own >= 256;
   p.tiles = p.rows ? own : (p.r_max + 16 * p.nb - 1) / (16 * p.nb);
   int64_t splits = 1;
