@@ -15,11 +15,13 @@
 // The pages' byte order gives each lane its 16 codes of an operand in one
 // 16-byte load, 1 KB in a row for a wave.
 //
-// Two ways to cut the work, by size (attend_plan): with few rows the four
-// waves of a workgroup share the rows and take every fourth block, the blocks
-// are split over workgroups as well, and partial sums are joined in a fixed
-// order (in LDS, then in k_attend_join); with many rows each wave has rows
-// of its own and walks all the blocks they see.
+// Two ways to cut the work, by size (attend_plan).  Few rows (k_attend): the
+// pages' bytes bound the time; the four waves of a workgroup share the rows
+// and take every fourth block.  Many rows (k_attend_many): the weights' exponentials and the
+// products do; each wave has rows of its own and all walk the blocks in
+// step, whose codes are turned to fp16 once for the workgroup, in LDS.  Both
+// split the blocks over workgroups as well where the rows do not fill the
+// CUs; partial sums are joined in a fixed order (in LDS, then in k_attend_join).
 #include "attn_device.h"
 
 namespace pi {
@@ -31,6 +33,8 @@ typedef float f32x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kAtThreads = 256;
 constexpr int kAtWaves = kAtThreads / kWave;
+constexpr int kManyThreads = 512;
+constexpr int kManyWaves = kManyThreads / kWave;
 constexpr int kMaxSplits = 64;
 constexpr float kNoMax = -1e30f;     // reference before the first visible token
 // Weights are held times 2^6, and a lane's eight of a block may sum to 2^15
@@ -94,329 +98,514 @@ __device__ void nan_rows(const AttendArgs& a, const Seq& q, int h, int d, int64_
   }
 }
 
+// What a (sequence, kv head, split) walks, the same for its whole workgroup.
+struct Walk {
+  int pair, s, h, tile, split;
+  Seq q;
+  int rows, seen0;       // rows of the pair; tokens that its first row sees (may be < 1)
+  __device__ Walk(const AttendArgs& a) {
+    const int pairs = a.n_seqs * a.hk;
+    pair = blockIdx.x % pairs;
+    tile = blockIdx.x / pairs % a.tiles;
+    split = blockIdx.x / pairs / a.tiles;
+    s = pair / a.hk, h = pair % a.hk;
+    q = read_seq(a.lens, a.q_start, s, a.max_q, a.n_tok, a.max_len);
+    rows = q.n * a.group;
+    seen0 = q.len - q.n + 1;
+  }
+  // Tokens that row r sees.
+  __device__ int sees(const AttendArgs& a, int r) const {
+    const int v = seen0 + r / a.group;
+    return v < 0 ? 0 : v;
+  }
+  __device__ int64_t out_at(const AttendArgs& a, int r) const {
+    return (int64_t)(q.q0 + r / a.group) * a.o_ts + (int64_t)(h * a.group + r % a.group) * a.o_hs;
+  }
+};
+
+// Pages and scales of up to 64 blocks, lane i those of the i-th.
+struct Blocks {
+  int page;
+  float ks, lr, iv, unit;        // key scale; log2 of the weights' factor (and kBias), 1 / factor; the sums' unit
+  unsigned long long smalls;     // blocks whose unit is not 1
+
+  __device__ void find(const AttendArgs& a, int pair, int first, int step, int cnt, bool& bad) {
+    page = 0;
+    if (lane_id() < cnt) {
+      page = a.table[(int64_t)pair * a.max_blocks + first + lane_id() * step];
+      const bool none = (unsigned)page >= (unsigned)a.n_pages;
+      ks = none ? -1.f : 0.f;
+      page = none ? 0 : page;
+      bad |= none;
+    }
+  }
+  // Returns the largest value scale.
+  __device__ float read_scales(const AttendArgs& a, int cnt, float& vs) {
+    vs = 0.f;
+    float k = 0.f;
+    if (lane_id() < cnt) {
+      const float2 sc = reinterpret_cast<const float2*>(a.scales)[page];
+      k = ks < 0.f ? -1.f : sc.x, vs = sc.y;
+      // A scale that is no number: what sees the block is NaN, through its logits.
+      if (!(k >= 0.f && k < __builtin_inff() && vs >= 0.f && vs < __builtin_inff())) k = quiet_nan(), vs = 0.f;
+    }
+    ks = k;
+    float vmax = vs;
+#pragma unroll
+    for (int x = 32; x >= 1; x >>= 1) vmax = fmaxf(vmax, __shfl_xor(vmax, x, kWave));
+    return vmax;
+  }
+  __device__ void set_units(float vs, float vref) {
+    const float ratio = vs > 0.f ? vs / vref : 1.f;
+    smalls = __ballot(ratio < kSmall);
+    unit = ratio < kSmall ? as_f(__builtin_bit_cast(unsigned, fmaxf(ratio, kSmallest)) & 0x7f800000u) : 1.f;
+    const float share = fmaxf(ratio / unit, 0x1p-60f);
+    lr = log2_hw(share) + kBias, iv = 1.f / share;
+  }
+};
+
+// NB * 16 rows of a wave: queries, running reference and sums.  T: fp16, or fp32 as
+// two fp16 parts; TWOP: the weights as two fp16 parts too.
+template <typename T, int D, int NB, bool SCORE, bool TWOP>
+struct Rows {
+  static constexpr int KK = D / 64, DT = D / 16;
+  static constexpr bool kTwo = sizeof(T) == 4;
+  int r0;
+  f16x8 qf[NB][KK][2], ql[NB][kTwo ? KK : 1][2];   // lane (g, c): elements 64 kk + 16 g .. + 16 of row c
+  float rs[NB];                                    // a row's power of two (fp32 rows)
+  int sees[NB];
+  f32x4 o[NB][DT];
+  float m[NB], l[NB];
+  float vref;                                      // o is in units of it
+
+  __device__ __forceinline__ void load(const AttendArgs& a, const Walk& w, int first) {
+    r0 = first;
+    const int lane = lane_id(), g = lane / 16, c = lane % 16;
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      const int r = r0 + nb * 16 + c;
+      const bool in = r < w.rows;
+      const int t = in ? r / a.group : 0, head = w.h * a.group + (in ? r % a.group : 0);
+      const T* p = static_cast<const T*>(a.q) + (int64_t)(w.q.q0 + t) * a.q_ts + (int64_t)head * a.q_hs + 16 * g;
+      sees[nb] = in ? w.sees(a, r) : 0;
+      rs[nb] = 1.f;
+      if constexpr (!kTwo) {
+#pragma unroll
+        for (int kk = 0; kk < KK; ++kk)
+#pragma unroll
+          for (int f = 0; f < 2; ++f) {
+            u32x4 v = {0, 0, 0, 0};
+            if (in) v = ld16(p + 64 * kk + 8 * f);
+            qf[nb][kk][f] = __builtin_bit_cast(f16x8, v);
+          }
+      } else {
+        float x[KK][16];
+        float top = 0.f;
+#pragma unroll
+        for (int kk = 0; kk < KK; ++kk)
+#pragma unroll
+          for (int f = 0; f < 4; ++f) {
+            u32x4 v = {0, 0, 0, 0};
+            if (in) v = ld16(p + 64 * kk + 4 * f);
+            Vec<float>::unpack(v, &x[kk][4 * f]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) top = fmaxf(top, __builtin_fabsf(x[kk][4 * f + i]));
+          }
+        top = row_max(top);
+        // The row times 2^-e lies below 2^14: both parts are normal fp16 numbers to 2^-38 of the largest.
+        int e = 0;
+        if (top > 0.f && top < __builtin_inff()) e = __builtin_amdgcn_frexp_expf(top) - 14;
+        e = e < -126 ? -126 : e;
+        rs[nb] = __builtin_amdgcn_ldexpf(1.f, e);
+#pragma unroll
+        for (int kk = 0; kk < KK; ++kk)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float v = __builtin_amdgcn_ldexpf(x[kk][i], -e);
+            const f16 hi = (f16)v;
+            qf[nb][kk][i / 8][i % 8] = hi;
+            ql[nb][kk][i / 8][i % 8] = (f16)(v - (float)hi);
+          }
+      }
+    }
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      m[nb] = kNoMax, l[nb] = 0.f;
+#pragma unroll
+      for (int t = 0; t < DT; ++t) o[nb][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+    vref = 0x1p-126f;
+  }
+
+  __device__ __forceinline__ void rescale(float f) {
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int t = 0; t < DT; ++t) o[nb][t] *= f;
+  }
+
+  // The sums' unit follows the largest value scale, a power of two.
+  __device__ __forceinline__ void raise_unit(float vmax) {
+    const float top = as_f(__builtin_bit_cast(unsigned, fmaxf(vmax, 0x1p-126f)) & 0x7f800000u);
+    if (top > vref) {
+      rescale(vref / top);
+      vref = top;
+    }
+  }
+
+  // Block b, the i-th of x.  keys(mb, kk, f) and values(t) give the operands;
+  // keys_done() is called when the last of the keys has been taken.  All the rows see
+  // the first `whole` tokens.
+  template <typename K, typename KD, typename V>
+  __device__ __forceinline__ void block(const AttendArgs& a, const Walk& w, const Blocks& x, int i, int b, int whole,
+                                        K keys, KD keys_done, V values) {
+    const int lane = lane_id(), g = lane / 16, c = lane % 16;
+    f32x4 st[NB][2];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) st[nb][0] = st[nb][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int kk = 0; kk < KK; ++kk)
+#pragma unroll
+      for (int f = 0; f < 2; ++f)
+#pragma unroll
+        for (int mb = 0; mb < 2; ++mb) {
+          const f16x8 kf = keys(mb, kk, f);
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) {
+            st[nb][mb] = mfma16(kf, qf[nb][kk][f], st[nb][mb]);
+            if constexpr (kTwo) st[nb][mb] = mfma16(kf, ql[nb][kk][f], st[nb][mb]);
+          }
+        }
+    keys_done();
+    const float ksc = lane_f(x.ks, i) * a.scale;
+    const float lrb = lane_f(x.lr, i), ivb = lane_f(x.iv, i);
+    const bool edge = (b + 1) * kBlk > whole;      // some row does not see all of the block
+    auto scale_of = [&](int nb) { return kTwo ? ksc * rs[nb] : ksc; };
+    if (edge) {
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        const float sc = scale_of(nb);
+        const int left = sees[nb] - b * kBlk - 4 * g;
+#pragma unroll
+        for (int mb = 0; mb < 2; ++mb)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) st[nb][mb][j] = mb * 16 + j < left ? st[nb][mb][j] * sc : -__builtin_inff();
+      }
+    }
+    f16x8 pf[NB], pl[NB];
+    float sum[NB];
+    auto weights = [&](int nb) {
+      const float sc = edge ? 1.f : scale_of(nb), off = lrb - m[nb];
+      float p[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) p[j] = exp2_hw(__builtin_fmaf(st[nb][j / 4][j % 4], sc, off));
+      const f32x8 pv = {p[0], p[1], p[2], p[3], p[4], p[5], p[6], p[7]};
+      pf[nb] = __builtin_convertvector(pv, f16x8);
+      if constexpr (TWOP) pl[nb] = __builtin_convertvector(pv - __builtin_convertvector(pf[nb], f32x8), f16x8);
+      if constexpr (TWOP || SCORE) {
+        sum[nb] = (p[0] + p[1] + (p[2] + p[3])) + (p[4] + p[5] + (p[6] + p[7]));
+      } else {
+        // the sum of the rounded weights, which the second product multiplies
+        const u32x4 v = __builtin_bit_cast(u32x4, pf[nb]);
+        const f16x2 one = {(f16)1.f, (f16)1.f};
+        float y = __builtin_amdgcn_fdot2(as_h2(v.x), one, 0.f, false);
+        y = __builtin_amdgcn_fdot2(as_h2(v.y), one, y, false);
+        y = __builtin_amdgcn_fdot2(as_h2(v.z), one, y, false);
+        sum[nb] = __builtin_amdgcn_fdot2(as_h2(v.w), one, y, false);
+      }
+    };
+    bool over = false;
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      weights(nb);
+      over |= !(sum[nb] < kMost);
+    }
+    if (__any(over)) {                             // a weight passes the reference by too much: move it
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        const f32x4 s0 = st[nb][0], s1 = st[nb][1];
+        const float top = fmaxf(fmaxf(fmaxf(s0[0], s0[1]), fmaxf(s0[2], s0[3])),
+                                fmaxf(fmaxf(s1[0], s1[1]), fmaxf(s1[2], s1[3]))) * (edge ? 1.f : scale_of(nb));
+        const float mn = fmaxf(m[nb], row_max(top));
+        const float f = exp2_hw(m[nb] - mn);
+        m[nb] = mn;
+        l[nb] *= f;
+#pragma unroll
+        for (int t = 0; t < DT; ++t) o[nb][t] *= f;
+        weights(nb);
+      }
+    }
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      l[nb] = __builtin_fmaf(sum[nb], ivb, l[nb]);
+      if constexpr (SCORE) {
+        const float bw = row_sum(sum[nb]) * ivb;
+        const int r = r0 + nb * 16 + c;
+        if (g == 0 && r < w.rows) a.lse[((int64_t)w.pair * a.max_nb + b) * a.r_max + r] = m[nb] + log2_hw(bw);
+      }
+    }
+    const bool far = x.smalls >> i & 1;
+    if (far) rescale(1.f / lane_f(x.unit, i));
+#pragma unroll
+    for (int t = 0; t < DT; ++t) {
+      const f16x8 v = values(t);
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        o[nb][t] = mfma16(v, pf[nb], o[nb][t]);
+        if constexpr (TWOP) o[nb][t] = mfma16(v, pl[nb], o[nb][t]);
+      }
+    }
+    if (far) rescale(lane_f(x.unit, i));
+  }
+
+  __device__ __forceinline__ void finish() {
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) l[nb] = row_sum(l[nb]);
+    rescale(vref);
+  }
+};
+
+// Four elements of a row, from fp32.
+template <typename T>
+__device__ __forceinline__ void store4(T* p, f32x4 v) {
+  if constexpr (sizeof(T) == 4) *reinterpret_cast<f32x4*>(p) = v;
+  else *reinterpret_cast<f16x4*>(p) = __builtin_convertvector(v, f16x4);
+}
+
 // Waves that a SIMD holds: what the registers of a wave's rows leave.
 constexpr int waves_per_simd(int d, int nb, bool f32) {
   return d * nb * (f32 ? 2 : 1) <= 64 ? 4 : (d * nb * (f32 ? 2 : 1) <= 128 ? 3 : 2);
 }
 
-// T: rows (fp16; fp32 as two fp16 parts).  NB: 16-row tiles of a wave.
-// SCORE: the weights of each block are wanted.  ROWS: see above.
-template <typename T, int D, int NB, bool SCORE, bool ROWS>
+template <typename T, int D, int NB, bool SCORE>
 __global__ __launch_bounds__(kAtThreads, waves_per_simd(D, NB, sizeof(T) == 4)) void k_attend(AttendArgs a) {
   constexpr int KK = D / 64, DT = D / 16, DB = D / 32;
-  constexpr bool kTwo = sizeof(T) == 4;             // two fp16 parts of q
-  constexpr bool kTwoP = kTwo || !ROWS;             // and of p: always where the pages' bytes bound the time
-  const int pairs = a.n_seqs * a.hk;
-  const int pair = blockIdx.x % pairs;
-  const int tile = blockIdx.x / pairs % a.tiles;
-  const int split = blockIdx.x / pairs / a.tiles;
-  const int s = pair / a.hk, h = pair % a.hk;
+  const Walk w(a);
   const int lane = lane_id(), wave = wave_id(), g = lane / 16, c = lane % 16;
-  const Seq q = read_seq(a.lens, a.q_start, s, a.max_q, a.n_tok, a.max_len);
-  if (!q.ok) {
-    if (split == 0) nan_rows<T>(a, q, h, D, (int64_t)tile * kAtThreads + threadIdx.x, (int64_t)a.tiles * kAtThreads);
+  if (!w.q.ok) {
+    if (w.split == 0) nan_rows<T>(a, w.q, w.h, D, (int64_t)w.tile * kAtThreads + threadIdx.x, (int64_t)a.tiles * kAtThreads);
     if (threadIdx.x == 0) raise_flag(a.flags, PI_FLAG_KV_RANGE);
     return;
   }
-  const int rows = q.n * a.group;
-  const int r0 = tile * 16 * NB;
-  if (r0 >= rows) return;
-  const int seen0 = q.len - q.n + 1;                // tokens that the sequence's first row sees (may be < 1)
-  const int r1 = r0 + 16 * NB < rows ? r0 + 16 * NB : rows;
-  auto clamp_len = [&](int v) { return v < 0 ? 0 : v; };
-  const int kmin = clamp_len(seen0 + r0 / a.group), kmax = clamp_len(seen0 + (r1 - 1) / a.group);
+  const int r0 = w.tile * 16 * NB;
+  if (r0 >= w.rows) return;
+  const int r1 = r0 + 16 * NB < w.rows ? r0 + 16 * NB : w.rows;
+  const int kmin = w.sees(a, r0), kmax = w.sees(a, r1 - 1);
   const int nbk = (kmax + kBlk - 1) / kBlk;
   const int per = (nbk + a.splits - 1) / a.splits;
-  const int b0 = split * per, b1 = b0 + per < nbk ? b0 + per : nbk;
-  constexpr int kStep = kAtWaves;
+  const int b0 = w.split * per, b1 = b0 + per < nbk ? b0 + per : nbk;
   const int start = b0 + wave;
-  const int mine = start < b1 ? (b1 - start + kStep - 1) / kStep : 0;
+  const int mine = start < b1 ? (b1 - start + kAtWaves - 1) / kAtWaves : 0;
 
-  // Queries: lane (g, c) has elements 64 kk + 16 g .. + 16 of row c.
-  f16x8 qf[NB][KK][2], ql[NB][kTwo ? KK : 1][2];
-  float rs[NB];                                     // a row's power of two (fp32 rows)
-  int sees[NB];
-#pragma unroll
-  for (int nb = 0; nb < NB; ++nb) {
-    const int r = r0 + nb * 16 + c;
-    const bool in = r < rows;
-    const int t = in ? r / a.group : 0, head = h * a.group + (in ? r % a.group : 0);
-    const T* p = static_cast<const T*>(a.q) + (int64_t)(q.q0 + t) * a.q_ts + (int64_t)head * a.q_hs + 16 * g;
-    sees[nb] = in ? clamp_len(seen0 + t) : 0;
-    rs[nb] = 1.f;
-    if constexpr (!kTwo) {
-#pragma unroll
-      for (int kk = 0; kk < KK; ++kk)
-#pragma unroll
-        for (int f = 0; f < 2; ++f) {
-          u32x4 v = {0, 0, 0, 0};
-          if (in) v = ld16(p + 64 * kk + 8 * f);
-          qf[nb][kk][f] = __builtin_bit_cast(f16x8, v);
-        }
-    } else {
-      float x[KK][16];
-      float top = 0.f;
-#pragma unroll
-      for (int kk = 0; kk < KK; ++kk)
-#pragma unroll
-        for (int f = 0; f < 4; ++f) {
-          u32x4 v = {0, 0, 0, 0};
-          if (in) v = ld16(p + 64 * kk + 4 * f);
-          Vec<float>::unpack(v, &x[kk][4 * f]);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) top = fmaxf(top, __builtin_fabsf(x[kk][4 * f + i]));
-        }
-      top = row_max(top);
-      // The row times 2^-e lies below 2^14: both parts are normal fp16 numbers to 2^-38 of the largest.
-      int e = 0;
-      if (top > 0.f && top < __builtin_inff()) e = __builtin_amdgcn_frexp_expf(top) - 14;
-      rs[nb] = __builtin_amdgcn_ldexpf(1.f, e < -126 ? -126 : e);
-#pragma unroll
-      for (int kk = 0; kk < KK; ++kk)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float v = __builtin_amdgcn_ldexpf(x[kk][i], -(e < -126 ? -126 : e));
-          const f16 hi = (f16)v;
-          qf[nb][kk][i / 8][i % 8] = hi;
-          ql[nb][kk][i / 8][i % 8] = (f16)(v - (float)hi);
-        }
-    }
-  }
-
-  f32x4 o[NB][DT];
-  float m[NB], l[NB];
-#pragma unroll
-  for (int nb = 0; nb < NB; ++nb) {
-    m[nb] = kNoMax, l[nb] = 0.f;
-#pragma unroll
-    for (int t = 0; t < DT; ++t) o[nb][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-  }
-  float vref = 0x1p-126f;                           // o is in units of it
-
+  // The weights as two parts: the products have time while the pages come.
+  Rows<T, D, NB, SCORE, true> rows;
+  rows.load(a, w, r0);
   u32x4 rk[2 * KK], rv[DB];                         // a block's codes, as they lie in the page
   bool bad = false;
+  Blocks x;
   for (int base = 0; base < mine; base += kWave) {
     const int cnt = mine - base < kWave ? mine - base : kWave;
-    // Lane i: page and scales of the i-th block.
-    int page = 0;
-    float ks = 0.f, vs = 0.f;
-    bool no_page = false;
-    if (lane < cnt) {
-      page = a.table[(int64_t)pair * a.max_blocks + start + (base + lane) * kStep];
-      no_page = (unsigned)page >= (unsigned)a.n_pages;
-      page = no_page ? 0 : page;
-      bad |= no_page;
-    }
+    x.find(a, w.pair, start + base * kAtWaves, kAtWaves, cnt, bad);
     auto page_at = [&](int i) {
-      return a.pages + (int64_t)__builtin_amdgcn_readlane(page, i) * (2 * kBlk * D) + lane * 16;
+      return a.pages + (int64_t)__builtin_amdgcn_readlane(x.page, i) * (2 * kBlk * D) + lane * 16;
     };
     auto load_k = [&](int i) {
       const uint8_t* p = page_at(i);
 #pragma unroll
-      for (int u = 0; u < 2 * KK; ++u) rk[u] = ROWS ? ld16(p + u * 1024) : ld_nt(p + u * 1024);
+      for (int u = 0; u < 2 * KK; ++u) rk[u] = ld_nt(p + u * 1024);
     };
     auto load_v = [&](int i) {
       const uint8_t* p = page_at(i) + kBlk * D;
 #pragma unroll
-      for (int u = 0; u < DB; ++u) rv[u] = ROWS ? ld16(p + u * 1024) : ld_nt(p + u * 1024);
+      for (int u = 0; u < DB; ++u) rv[u] = ld_nt(p + u * 1024);
     };
     // The first block's codes are on their way while the scales come.
     load_k(0);
     load_v(0);
-    if (lane < cnt) {
-      const float2 sc = reinterpret_cast<const float2*>(a.scales)[page];
-      ks = no_page ? -1.f : sc.x, vs = sc.y;
-      // A scale that is no number: what sees the block is NaN, through its logits.
-      if (!(ks >= 0.f && ks < __builtin_inff() && vs >= 0.f && vs < __builtin_inff())) ks = quiet_nan(), vs = 0.f;
-    }
-    float vmax = vs;
-#pragma unroll
-    for (int x = 32; x >= 1; x >>= 1) vmax = fmaxf(vmax, __shfl_xor(vmax, x, kWave));
-    const float vtop = as_f(__builtin_bit_cast(unsigned, fmaxf(vmax, 0x1p-126f)) & 0x7f800000u);
-    if (vtop > vref) {
-      const float f = vref / vtop;
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-        for (int t = 0; t < DT; ++t) o[nb][t] *= f;
-      vref = vtop;
-    }
-    const float ratio = vs > 0.f ? vs / vref : 1.f;
-    const unsigned long long smalls = __ballot(ratio < kSmall);
-    const float unit = ratio < kSmall ? as_f(__builtin_bit_cast(unsigned, fmaxf(ratio, kSmallest)) & 0x7f800000u) : 1.f;
-    const float share = fmaxf(ratio / unit, 0x1p-60f);
-    const float lr = log2_hw(share) + kBias, iv = 1.f / share;
-
+    float vs;
+    rows.raise_unit(x.read_scales(a, cnt, vs));
+    x.set_units(vs, rows.vref);
     // One set of registers for the codes: the next block's keys are on their
     // way from the end of the first product on, its values from the second's.
-    for (int i = 0; i < cnt; ++i) {
-      const int b = start + (base + i) * kStep;
-      const float ksc = lane_f(ks, i) * a.scale;
-      const float lrb = lane_f(lr, i), ivb = lane_f(iv, i);
-      f32x4 st[NB][2];
+    // (The last block is a step of its own: loads under a condition would be
+    // waited for as if they had not been issued.)
+    auto step = [&](int i, auto more) {
+      rows.block(
+          a, w, x, i, start + (base + i) * kAtWaves, kmin,
+          [&](int mb, int kk, int f) {
+            const u32x4 v = rk[mb * KK + kk];
+            return f ? codes_f16(v.z, v.w) : codes_f16(v.x, v.y);
+          },
+          [&] {
+            if constexpr (decltype(more)::value) load_k(i + 1);
+          },
+          [&](int t) {
+            const u32x4 v = rv[t / 2];
+            return t % 2 ? codes_f16(v.z, v.w) : codes_f16(v.x, v.y);
+          });
+      if constexpr (decltype(more)::value) load_v(i + 1);
+    };
+    for (int i = 0; i + 1 < cnt; ++i) step(i, std::true_type());
+    step(cnt - 1, std::false_type());
+  }
+  raise_flag_if_any(a.flags, bad, PI_FLAG_KV_RANGE);
+  rows.finish();
+
+  // The four waves' sums, added in wave order.
+  __shared__ float so[kAtWaves][16][D + 4];
+  __shared__ float sm[kAtWaves][16], sl[kAtWaves][16];
+  constexpr int E = D / 16;                         // elements of a thread
+  const int row = threadIdx.x / 16, e0 = threadIdx.x % 16 * E;
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb) st[nb][0] = st[nb][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int nb = 0; nb < NB; ++nb) {
+    if (nb) __syncthreads();
 #pragma unroll
-      for (int kk = 0; kk < KK; ++kk)
+    for (int t = 0; t < DT; ++t) *reinterpret_cast<f32x4*>(&so[wave][c][16 * t + 4 * g]) = rows.o[nb][t];
+    if (g == 0) sm[wave][c] = rows.m[nb], sl[wave][c] = rows.l[nb];
+    __syncthreads();
+    const int r = r0 + nb * 16 + row;
+    if (r >= w.rows) continue;
+    float top = sm[0][row];
 #pragma unroll
-        for (int f = 0; f < 2; ++f)
+    for (int y = 1; y < kAtWaves; ++y) top = fmaxf(top, sm[y][row]);
+    float sum = 0.f, v[E];
 #pragma unroll
-          for (int mb = 0; mb < 2; ++mb) {
-            const u32x4 w = rk[mb * KK + kk];
-            const f16x8 kf = f ? codes_f16(w.z, w.w) : codes_f16(w.x, w.y);
+    for (int k = 0; k < E; ++k) v[k] = 0.f;
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb) {
-              st[nb][mb] = mfma16(kf, qf[nb][kk][f], st[nb][mb]);
-              if constexpr (kTwo) st[nb][mb] = mfma16(kf, ql[nb][kk][f], st[nb][mb]);
-            }
-          }
-      if (i + 1 < cnt) load_k(i + 1);
-      const bool edge = (b + 1) * kBlk > kmin;      // some row does not see all of the block
-      auto scale_of = [&](int nb) { return kTwo ? ksc * rs[nb] : ksc; };
-      if (edge) {
+    for (int y = 0; y < kAtWaves; ++y) {
+      const float f = exp2_hw(sm[y][row] - top);
+      sum = __builtin_fmaf(f, sl[y][row], sum);
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-          const float sc = scale_of(nb);
+      for (int k = 0; k < E; ++k) v[k] = __builtin_fmaf(f, so[y][row][e0 + k], v[k]);
+    }
+    const int64_t at = ((int64_t)w.split * a.n_seqs * a.hk + w.pair) * a.r_max + r;
+    const bool whole = a.splits == 1;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    T* p = static_cast<T*>(a.out) + w.out_at(a, r) + e0;
 #pragma unroll
-          for (int mb = 0; mb < 2; ++mb)
+    for (int k = 0; k < E; k += 4) {
+      const f32x4 y = {v[k], v[k + 1], v[k + 2], v[k + 3]};
+      if (whole) store4(p + k, y * inv);
+      else *reinterpret_cast<f32x4*>(a.part + at * D + e0 + k) = y;
+    }
+    if ((!whole || SCORE) && e0 == 0) a.ml[at] = float2{top, sum};
+  }
+}
+
+// NB * 16 rows to a wave, kManyWaves waves to a group; the G groups share the
+// rows and take every G-th step.  The codes of a step's blocks become fp16
+// operands in LDS once for all of them: a wave turns one unit (1 KB of a page)
+// per step, and the next step's units are on their way meanwhile.
+template <typename T, int D, int NB, bool SCORE, int G>
+__global__ __launch_bounds__(G * kManyThreads, 2 * G) void k_attend_many(AttendArgs a) {
+  constexpr int KK = D / 64, DT = D / 16, kUnits = D / 16, kPart = kManyWaves / kUnits, kStep = G * kPart;
+  constexpr int kThreads = G * kManyThreads;
+  const Walk w(a);
+  const int lane = lane_id(), g = lane / 16, c = lane % 16;
+  const int wave = wave_id() % kManyWaves, group = wave_id() / kManyWaves;
+  if (!w.q.ok) {
+    if (w.split == 0) nan_rows<T>(a, w.q, w.h, D, (int64_t)w.tile * kThreads + threadIdx.x, (int64_t)a.tiles * kThreads);
+    if (threadIdx.x == 0) raise_flag(a.flags, PI_FLAG_KV_RANGE);
+    return;
+  }
+  constexpr int kRows = 16 * NB * kManyWaves;
+  // The last rows see the most: they begin first.
+  const int g0 = (a.tiles - 1 - w.tile) * kRows;
+  if (g0 >= w.rows) return;
+  const int g1 = g0 + kRows < w.rows ? g0 + kRows : w.rows;
+  const int nbk = (w.sees(a, g1 - 1) + kBlk - 1) / kBlk;
+  const int per = (nbk + a.splits - 1) / a.splits;
+  const int b0 = w.split * per, b1 = b0 + per < nbk ? b0 + per : nbk;
+  const int r0 = g0 + wave * 16 * NB;
+  const int r1 = r0 + 16 * NB < w.rows ? r0 + 16 * NB : w.rows;
+  const int kmin = r0 < w.rows ? w.sees(a, r0) : 0, kmax = r0 < w.rows ? w.sees(a, r1 - 1) : 0;
+
+  __shared__ u32x4 ops[2][kStep][kUnits][2][kWave];
+  Rows<T, D, NB, SCORE, sizeof(T) == 4> rows;
+  rows.load(a, w, r0);
+  bool bad = false;
+  Blocks x;
+  const int sj = wave_id() / kUnits, su = wave_id() % kUnits; // the unit that this wave turns
+  for (int base = b0; base < b1; base += kWave) {
+    const int cnt = b1 - base < kWave ? b1 - base : kWave;
+    x.find(a, w.pair, base, 1, cnt, bad);
+    auto fetch = [&](int i) {                        // of the step that begins with block i (past cnt: page 0, not used)
+      return ld16(a.pages + (int64_t)__builtin_amdgcn_readlane(x.page, i + sj) * (2 * kBlk * D) + su * 1024 + lane * 16);
+    };
+    auto turn = [&](int buf, u32x4 v) {
+      ops[buf][sj][su][0][lane] = __builtin_bit_cast(u32x4, codes_f16(v.x, v.y));
+      ops[buf][sj][su][1][lane] = __builtin_bit_cast(u32x4, codes_f16(v.z, v.w));
+    };
+    u32x4 next = fetch(0);
+    float vs;
+    rows.raise_unit(x.read_scales(a, cnt, vs));
+    x.set_units(vs, rows.vref);
+    turn(0, next);
+    __syncthreads();
+    int buf = 0;
+    for (int i = 0; i < cnt; i += kStep) {
+      const bool more = i + kStep < cnt;
+      if (more) next = fetch(i + kStep);
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              st[nb][mb][j] = b * kBlk + mb * 16 + 4 * g + j < sees[nb] ? st[nb][mb][j] * sc : -__builtin_inff();
-        }
+      for (int y = 0; y < kPart; ++y) {
+        const int j = group * kPart + y, b = base + i + j;
+        if (i + j < cnt && b * kBlk < kmax)
+          rows.block(
+              a, w, x, i + j, b, kmin,
+              [&](int mb, int kk, int f) { return __builtin_bit_cast(f16x8, ops[buf][j][mb * KK + kk][f][lane]); }, [] {},
+              [&](int t) { return __builtin_bit_cast(f16x8, ops[buf][j][2 * KK + t / 2][t % 2][lane]); });
       }
-      f16x8 pf[NB], pl[NB];
-      float sum[NB];
-      auto weights = [&](int nb) {
-        const float sc = edge ? 1.f : scale_of(nb), off = lrb - m[nb];
-        float p[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) p[j] = exp2_hw(__builtin_fmaf(st[nb][j / 4][j % 4], sc, off));
-        const f32x8 pv = {p[0], p[1], p[2], p[3], p[4], p[5], p[6], p[7]};
-        pf[nb] = __builtin_convertvector(pv, f16x8);
-        if constexpr (kTwoP) pl[nb] = __builtin_convertvector(pv - __builtin_convertvector(pf[nb], f32x8), f16x8);
-        if constexpr (kTwoP || SCORE) {
-          sum[nb] = (p[0] + p[1] + (p[2] + p[3])) + (p[4] + p[5] + (p[6] + p[7]));
-        } else {
-          // the sum of the rounded weights, which the second product multiplies
-          const u32x4 w = __builtin_bit_cast(u32x4, pf[nb]);
-          const f16x2 one = {(f16)1.f, (f16)1.f};
-          float x = __builtin_amdgcn_fdot2(as_h2(w.x), one, 0.f, false);
-          x = __builtin_amdgcn_fdot2(as_h2(w.y), one, x, false);
-          x = __builtin_amdgcn_fdot2(as_h2(w.z), one, x, false);
-          sum[nb] = __builtin_amdgcn_fdot2(as_h2(w.w), one, x, false);
-        }
-      };
-      bool over = false;
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb) {
-        weights(nb);
-        over |= !(sum[nb] < kMost);
-      }
-      if (__any(over)) {                            // a weight passes the reference by too much: move it
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-          const f32x4 s0 = st[nb][0], s1 = st[nb][1];
-          const float top = fmaxf(fmaxf(fmaxf(s0[0], s0[1]), fmaxf(s0[2], s0[3])),
-                                  fmaxf(fmaxf(s1[0], s1[1]), fmaxf(s1[2], s1[3]))) * (edge ? 1.f : scale_of(nb));
-          const float mn = fmaxf(m[nb], row_max(top));
-          const float f = exp2_hw(m[nb] - mn);
-          m[nb] = mn;
-          l[nb] *= f;
-#pragma unroll
-          for (int t = 0; t < DT; ++t) o[nb][t] *= f;
-          weights(nb);
-        }
-      }
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb) {
-        l[nb] = __builtin_fmaf(sum[nb], ivb, l[nb]);
-        if constexpr (SCORE) {
-          const float w = row_sum(sum[nb]) * ivb;
-          const int r = r0 + nb * 16 + c;
-          if (g == 0 && r < rows) a.lse[((int64_t)pair * a.max_nb + b) * a.r_max + r] = m[nb] + log2_hw(w);
-        }
-      }
-      auto rescale = [&](float f) {
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-          for (int t = 0; t < DT; ++t) o[nb][t] *= f;
-      };
-      const bool far = smalls >> i & 1;
-      if (far) rescale(1.f / lane_f(unit, i));
-#pragma unroll
-      for (int t = 0; t < DT; ++t) {
-        const u32x4 w = rv[t / 2];
-        const f16x8 v = t % 2 ? codes_f16(w.z, w.w) : codes_f16(w.x, w.y);
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-          o[nb][t] = mfma16(v, pf[nb], o[nb][t]);
-          if constexpr (kTwoP) o[nb][t] = mfma16(v, pl[nb], o[nb][t]);
-        }
-      }
-      if (far) rescale(lane_f(unit, i));
-      if (i + 1 < cnt) load_v(i + 1);
+      buf ^= 1;
+      if (more) turn(buf, next);
+      __syncthreads();                               // this step's operands are free, the next one's there
     }
   }
   raise_flag_if_any(a.flags, bad, PI_FLAG_KV_RANGE);
-
+  rows.finish();
+  if constexpr (G > 1) {
+    // The groups' sums, in the order of the groups; a lane's elements are the same in each.
+    __shared__ float2 sml[kManyWaves][NB][kWave];
+    static_assert(sizeof(ops) >= sizeof(f32x4) * kManyWaves * NB * DT * kWave, "a group's sums fit the operands' place");
+    f32x4* so = &reinterpret_cast<f32x4*>(ops)[(wave * NB * DT) * kWave + lane];
+    for (int y = 1; y < G; ++y) {
+      if (group == y) {
 #pragma unroll
-  for (int nb = 0; nb < NB; ++nb) {
-    l[nb] = row_sum(l[nb]);
+        for (int nb = 0; nb < NB; ++nb) {
+          sml[wave][nb][lane] = float2{rows.m[nb], rows.l[nb]};
 #pragma unroll
-    for (int t = 0; t < DT; ++t) o[nb][t] *= vref;
-  }
-  auto out_row = [&](int r) {
-    return static_cast<T*>(a.out) + (int64_t)(q.q0 + r / a.group) * a.o_ts + (int64_t)(h * a.group + r % a.group) * a.o_hs;
-  };
-  {
-    // The four waves' sums, added in wave order.
-    __shared__ float so[kAtWaves][16][D + 4];
-    __shared__ float sm[kAtWaves][16], sl[kAtWaves][16];
-    constexpr int E = D / 16;                       // elements of a thread
-    const int row = threadIdx.x / 16, e0 = threadIdx.x % 16 * E;
-    for (int nb = 0; nb < NB; ++nb) {
-      if (nb) __syncthreads();
-#pragma unroll
-      for (int x = 0; x < NB; ++x) {
-        if (x != nb) continue;
-#pragma unroll
-        for (int t = 0; t < DT; ++t) *reinterpret_cast<f32x4*>(&so[wave][c][16 * t + 4 * g]) = o[x][t];
-        if (g == 0) sm[wave][c] = m[x], sl[wave][c] = l[x];
-      }
-      __syncthreads();
-      const int r = r0 + nb * 16 + row;
-      if (r >= rows) continue;
-      float top = sm[0][row];
-#pragma unroll
-      for (int w = 1; w < kAtWaves; ++w) top = fmaxf(top, sm[w][row]);
-      float sum = 0.f, v[E];
-#pragma unroll
-      for (int k = 0; k < E; ++k) v[k] = 0.f;
-#pragma unroll
-      for (int w = 0; w < kAtWaves; ++w) {
-        const float f = exp2_hw(sm[w][row] - top);
-        sum = __builtin_fmaf(f, sl[w][row], sum);
-#pragma unroll
-        for (int k = 0; k < E; ++k) v[k] = __builtin_fmaf(f, so[w][row][e0 + k], v[k]);
-      }
-      const int64_t at = ((int64_t)split * pairs + pair) * a.r_max + r;
-      if (a.splits > 1) {
-#pragma unroll
-        for (int k = 0; k < E; k += 4)
-          *reinterpret_cast<f32x4*>(a.part + at * D + e0 + k) = f32x4{v[k], v[k + 1], v[k + 2], v[k + 3]};
-      } else {
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        T* p = out_row(r) + e0;
-#pragma unroll
-        for (int k = 0; k < E; k += 4) {
-          const f32x4 x = f32x4{v[k], v[k + 1], v[k + 2], v[k + 3]} * inv;
-          if constexpr (kTwo) *reinterpret_cast<f32x4*>(p + k) = x;
-          else *reinterpret_cast<f16x4*>(p + k) = __builtin_convertvector(x, f16x4);
+          for (int t = 0; t < DT; ++t) so[(nb * DT + t) * kWave] = rows.o[nb][t];
         }
       }
-      if ((a.splits > 1 || SCORE) && e0 == 0) a.ml[at] = float2{top, sum};
+      __syncthreads();
+      if (group == 0) {
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          const float2 v = sml[wave][nb][lane];
+          const float top = fmaxf(rows.m[nb], v.x), f0 = exp2_hw(rows.m[nb] - top), f1 = exp2_hw(v.x - top);
+          rows.m[nb] = top;
+          rows.l[nb] = rows.l[nb] * f0 + v.y * f1;
+#pragma unroll
+          for (int t = 0; t < DT; ++t) rows.o[nb][t] = rows.o[nb][t] * f0 + so[(nb * DT + t) * kWave] * f1;
+        }
+      }
+      if (y + 1 < G) __syncthreads();
     }
+    if (group) return;
+  }
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb) {
+    const int r = r0 + nb * 16 + c;
+    if (r >= w.rows) continue;
+    const bool whole = a.splits == 1;
+    const int64_t at = ((int64_t)w.split * a.n_seqs * a.hk + w.pair) * a.r_max + r;
+    const float inv = rows.l[nb] == 0.f ? 0.f : 1.f / rows.l[nb];
+    T* p = static_cast<T*>(a.out) + w.out_at(a, r) + 4 * g;
+#pragma unroll
+    for (int t = 0; t < DT; ++t) {
+      if (whole) store4(p + 16 * t, rows.o[nb][t] * inv);
+      else *reinterpret_cast<f32x4*>(a.part + at * D + 16 * t + 4 * g) = rows.o[nb][t];
+    }
+    if ((!whole || SCORE) && g == 0) a.ml[at] = float2{rows.m[nb], rows.l[nb]};
   }
 }
 
@@ -432,15 +621,46 @@ __device__ __forceinline__ float2 row_ml(const AttendArgs& a, int pairs, int pai
   return v;
 }
 
-// Joins the splits' sums into rows (workgroups below row_groups, one a row)
-// and adds the blocks' weights to the score (the others, kScoreBlocks blocks
+// Joins the splits' sums into rows (workgroups below row_groups: kFewSplits
+// splits or less, a thread adds them and a workgroup takes as many rows as it has
+// threads for; more, a workgroup takes one row and shares the splits) and adds the blocks' weights to the score (the others, kScoreBlocks blocks
 // of a (sequence, kv head) each).
 constexpr int kScoreBlocks = 64;
+constexpr int kFewSplits = 8;
 template <typename T, int D>
 __global__ __launch_bounds__(kAtThreads) void k_attend_join(AttendArgs a, int row_groups) {
   const int pairs = a.n_seqs * a.hk;
   if ((int)blockIdx.x < row_groups) {
-    constexpr int L = D / 4, G = kAtThreads / L;    // lanes of a row, splits at a time
+    constexpr int L = D / 4, G = kAtThreads / L;    // lanes of a row, splits (or rows) at a time
+    if (a.splits <= kFewSplits) {
+      const int64_t id = (int64_t)blockIdx.x * G + threadIdx.x / L;
+      const int pair = (int)(id / a.r_max), r = (int)(id % a.r_max), e = threadIdx.x % L * 4;
+      if (pair >= pairs) return;
+      const Seq q = read_seq(a.lens, a.q_start, pair / a.hk, a.max_q, a.n_tok, a.max_len);
+      if (!q.ok || r >= q.n * a.group) return;
+      f32x4 x[kFewSplits];
+      float2 v[kFewSplits];
+      float top = kNoMax;
+#pragma unroll
+      for (int k = 0; k < kFewSplits; ++k) {
+        const int64_t at = ((int64_t)(k < a.splits ? k : 0) * pairs + pair) * a.r_max + r;
+        v[k] = a.ml[at];
+        x[k] = *reinterpret_cast<const f32x4*>(a.part + at * D + e);
+        top = fmaxf(top, v[k].x);
+      }
+      f32x4 o = {0.f, 0.f, 0.f, 0.f};
+      float sum = 0.f;
+#pragma unroll
+      for (int k = 0; k < kFewSplits; ++k) {
+        const float f = k < a.splits ? exp2_hw(v[k].x - top) : 0.f;
+        sum = __builtin_fmaf(f, v[k].y, sum);
+        o += k < a.splits ? f * x[k] : f32x4{0.f, 0.f, 0.f, 0.f};
+      }
+      const int h = pair % a.hk;
+      T* p = static_cast<T*>(a.out) + (int64_t)(q.q0 + r / a.group) * a.o_ts + (int64_t)(h * a.group + r % a.group) * a.o_hs;
+      store4(p + e, o * (sum == 0.f ? 0.f : 1.f / sum));
+      return;
+    }
     __shared__ f32x4 acc[G][L];
     const int pair = blockIdx.x / a.r_max, r = blockIdx.x % a.r_max;
     const Seq q = read_seq(a.lens, a.q_start, pair / a.hk, a.max_q, a.n_tok, a.max_len);
@@ -476,8 +696,7 @@ __global__ __launch_bounds__(kAtThreads) void k_attend_join(AttendArgs a, int ro
     o *= sum == 0.f ? 0.f : 1.f / sum;
     const int h = pair % a.hk;
     T* p = static_cast<T*>(a.out) + (int64_t)(q.q0 + r / a.group) * a.o_ts + (int64_t)(h * a.group + r % a.group) * a.o_hs + e;
-    if constexpr (sizeof(T) == 4) *reinterpret_cast<f32x4*>(p) = o;
-    else *reinterpret_cast<f16x4*>(p) = __builtin_convertvector(o, f16x4);
+    store4(p, o);
     return;
   }
   const int per = (a.max_nb + kScoreBlocks - 1) / kScoreBlocks;
@@ -508,32 +727,47 @@ __global__ __launch_bounds__(kAtThreads) void k_attend_join(AttendArgs a, int ro
   if (sub == 0 && b * kBlk < q.len) a.score[(int64_t)pair * a.max_blocks + b] += w;
 }
 
-template <typename T, int D, int NB, bool ROWS>
+// 16-row tiles of a wave, at most: what its registers hold beside the pages' codes.
+constexpr int max_tiles(int d, bool f32) { return d == 128 && f32 ? 1 : 2; }
+
+// k_attend up to so many rows, k_attend_many beyond.  Measured over 4000 to
+// 8000 tokens, 2 to 32 (sequence, kv head) pairs: fp16, D = 128, 8 pairs, 32 rows
+// 17.4 us here and 17.5 there, 64 rows 22.9 and 19.0, 256 rows 45.5 and 31.5;
+// fp32 (twice the products either way), D = 64, 128 rows 16.5 and 20.1, 256
+// rows 27.6 and 27.8, 512 rows 34.4 and 31.1.
+constexpr int most_rows_few(bool f32) { return f32 ? 256 : 32; }
+
+// Launches one of the two kernels (NB 0: k_attend_many) and the join.
+template <typename T, int D, int NB>
 hipError_t attend_run(const AttendArgs& a, hipStream_t s) {
   const int pairs = a.n_seqs * a.hk;
   const dim3 grid((unsigned)pairs * a.tiles * a.splits);
-  if (a.score) k_attend<T, D, NB, true, ROWS><<<grid, kAtThreads, 0, s>>>(a);
-  else k_attend<T, D, NB, false, ROWS><<<grid, kAtThreads, 0, s>>>(a);
+  if constexpr (NB == 0) {
+    // Two groups where the rows' registers leave room for four waves a SIMD.
+    constexpr int G = D == 64 && sizeof(T) == 2 ? 2 : 1;
+    constexpr int M = max_tiles(D, sizeof(T) == 4);
+    if (a.score) k_attend_many<T, D, M, true, 1><<<grid, kManyThreads, 0, s>>>(a);
+    else k_attend_many<T, D, M, false, G><<<grid, G * kManyThreads, 0, s>>>(a);
+  } else {
+    if (a.score) k_attend<T, D, NB, true><<<grid, kAtThreads, 0, s>>>(a);
+    else k_attend<T, D, NB, false><<<grid, kAtThreads, 0, s>>>(a);
+  }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || (a.splits == 1 && !a.score)) return e;
-  const int row_groups = a.splits > 1 ? pairs * a.r_max : 0;
+  const int each = a.splits <= kFewSplits ? kAtThreads / (D / 4) : 1;      // rows of a workgroup
+  const int row_groups = a.splits > 1 ? (int)(((int64_t)pairs * a.r_max + each - 1) / each) : 0;
   const int score_groups = a.score ? pairs * ((a.max_nb + kScoreBlocks - 1) / kScoreBlocks) : 0;
   k_attend_join<T, D><<<dim3((unsigned)row_groups + score_groups), kAtThreads, 0, s>>>(a, row_groups);
   return hipGetLastError();
 }
 
-// 16-row tiles that a wave's registers hold.
-constexpr int max_tiles(int d, bool f32) { return (d == 64 ? 4 : 2) / (f32 ? 2 : 1); }
-
 template <typename T, int D>
 hipError_t attend_nb(const AttendArgs& a, const AttendPlan& p, hipStream_t s) {
   constexpr int kMax = max_tiles(D, sizeof(T) == 4);
-  if (p.rows) return attend_run<T, D, kMax, true>(a, s);
-  if constexpr (kMax >= 4)
-    if (p.nb == 4) return attend_run<T, D, 4, false>(a, s);
+  if (p.many) return attend_run<T, D, 0>(a, s);
   if constexpr (kMax >= 2)
-    if (p.nb == 2) return attend_run<T, D, 2, false>(a, s);
-  return attend_run<T, D, 1, false>(a, s);
+    if (p.nb == 2) return attend_run<T, D, 2>(a, s);
+  return attend_run<T, D, 1>(a, s);
 }
 
 }  // namespace
@@ -546,17 +780,14 @@ AttendPlan attend_plan(int n_seqs, int hk, int group, int d, int dtype, int max_
   const int cap = max_tiles(d, dtype == PI_F32);
   p.nb = 1;
   while (p.nb < cap && p.nb * 16 < p.r_max) p.nb *= 2;
-  // Waves with rows of their own where that fills the waves and the CUs.
-  const int own = (p.r_max + 16 * cap - 1) / (16 * cap);
-  p.rows = p.r_max >= 16 * cap * kAtWaves && pairs * own >= 256;
-  p.tiles = p.rows ? own : (p.r_max + 16 * p.nb - 1) / (16 * p.nb);
-  int64_t splits = 1;
-  if (!p.rows) {
-    const int64_t want = (1024 + pairs * p.tiles - 1) / (pairs * p.tiles), most = (p.max_nb + 7) / 8;
-    splits = want < most ? want : most;
-    splits = splits < kMaxSplits ? splits : kMaxSplits;
-  }
-  p.splits = (int)splits;
+  p.many = p.r_max > most_rows_few(dtype == PI_F32);
+  const int wg_rows = p.many ? 16 * cap * kManyWaves : 16 * p.nb;
+  p.tiles = (p.r_max + wg_rows - 1) / wg_rows;
+  const int64_t wgs = pairs * p.tiles;
+  int64_t splits = ((p.many ? 256 : 1024) + wgs - 1) / wgs;
+  const int64_t most = (p.max_nb + 7) / 8;
+  splits = splits < most ? splits : most;
+  p.splits = (int)(splits < kMaxSplits ? splits : kMaxSplits);
   auto up256 = [](size_t v) { return (v + 255) & ~size_t(255); };
   size_t off = PI_WS_HEADER_BYTES;
   p.part = off;

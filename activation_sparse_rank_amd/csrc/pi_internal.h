@@ -278,7 +278,7 @@ hipError_t launch_kv_read(const CacheArgs& a, hipStream_t s);
 // How a pi_attend call is cut up (by sizes and types alone).
 struct AttendPlan {
   int nb;                   // 16-row tiles per wave
-  bool rows;                // each wave has rows of its own; else the waves of a workgroup share rows and split the blocks
+  bool many;                // each wave has rows of its own; else the waves of a workgroup share rows and split the blocks
   int tiles;                // workgroups over the rows of a (sequence, kv head)
   int splits;               // workgroups over the blocks
   int r_max;                // rows of a (sequence, kv head): max_q * group
