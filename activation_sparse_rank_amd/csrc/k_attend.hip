@@ -372,13 +372,8 @@ __device__ __forceinline__ void store4(T* p, f32x4 v) {
   else *reinterpret_cast<f16x4*>(p) = __builtin_convertvector(v, f16x4);
 }
 
-// Waves that a SIMD holds: what the registers of a wave's rows leave.
-constexpr int waves_per_simd(int d, int nb, bool f32) {
-  return d * nb * (f32 ? 2 : 1) <= 64 ? 4 : (d * nb * (f32 ? 2 : 1) <= 128 ? 3 : 2);
-}
-
 template <typename T, int D, int NB, bool SCORE>
-__global__ __launch_bounds__(kAtThreads, waves_per_simd(D, NB, sizeof(T) == 4)) void k_attend(AttendArgs a) {
+__global__ __launch_bounds__(kAtThreads, 2) void k_attend(AttendArgs a) {
   constexpr int KK = D / 64, DT = D / 16, DB = D / 32;
   const Walk w(a);
   const int lane = lane_id(), wave = wave_id(), g = lane / 16, c = lane % 16;
@@ -727,15 +722,16 @@ __global__ __launch_bounds__(kAtThreads) void k_attend_join(AttendArgs a, int ro
   if (sub == 0 && b * kBlk < q.len) a.score[(int64_t)pair * a.max_blocks + b] += w;
 }
 
-// 16-row tiles of a wave, at most: what its registers hold beside the pages' codes.
-constexpr int max_tiles(int d, bool f32) { return d == 128 && f32 ? 1 : 2; }
+// 16-row tiles of a wave: what its registers hold, beside the pages' codes in k_attend.
+constexpr int few_tiles(int d) { return d == 64 ? 2 : 1; }
+constexpr int many_tiles(int d, bool f32) { return d == 128 && f32 ? 1 : 2; }
 
-// k_attend up to so many rows, k_attend_many beyond.  Measured over 4000 to
-// 8000 tokens, 2 to 32 (sequence, kv head) pairs: fp16, D = 128, 8 pairs, 32 rows
-// 17.4 us here and 17.5 there, 64 rows 22.9 and 19.0, 256 rows 45.5 and 31.5;
-// fp32 (twice the products either way), D = 64, 128 rows 16.5 and 20.1, 256
-// rows 27.6 and 27.8, 512 rows 34.4 and 31.1.
-constexpr int most_rows_few(bool f32) { return f32 ? 256 : 32; }
+// k_attend up to so many rows, k_attend_many beyond.  Measured on one card: fp16, D =
+// 128, 4 sequences of 8192 tokens, 32 rows 45.5 us here (two tiles a wave) and
+// 36.7 there; D = 64, 32 rows over 8000 tokens 12.6 and 15.7 us, 64 rows 25.9
+// and 17.0; fp32 (twice the products either way), D = 64, 128 rows 16.5 and
+// 20.1, 256 rows 27.6 and 27.8, 512 rows 34.4 and 31.1.
+constexpr int most_rows_few(int d, bool f32) { return f32 ? 256 : 16 * few_tiles(d); }
 
 // Launches one of the two kernels (NB 0: k_attend_many) and the join.
 template <typename T, int D, int NB>
@@ -745,7 +741,7 @@ hipError_t attend_run(const AttendArgs& a, hipStream_t s) {
   if constexpr (NB == 0) {
     // Two groups where the rows' registers leave room for four waves a SIMD.
     constexpr int G = D == 64 && sizeof(T) == 2 ? 2 : 1;
-    constexpr int M = max_tiles(D, sizeof(T) == 4);
+    constexpr int M = many_tiles(D, sizeof(T) == 4);
     if (a.score) k_attend_many<T, D, M, true, 1><<<grid, kManyThreads, 0, s>>>(a);
     else k_attend_many<T, D, M, false, G><<<grid, G * kManyThreads, 0, s>>>(a);
   } else {
@@ -763,9 +759,8 @@ hipError_t attend_run(const AttendArgs& a, hipStream_t s) {
 
 template <typename T, int D>
 hipError_t attend_nb(const AttendArgs& a, const AttendPlan& p, hipStream_t s) {
-  constexpr int kMax = max_tiles(D, sizeof(T) == 4);
   if (p.many) return attend_run<T, D, 0>(a, s);
-  if constexpr (kMax >= 2)
+  if constexpr (few_tiles(D) == 2)
     if (p.nb == 2) return attend_run<T, D, 2>(a, s);
   return attend_run<T, D, 1>(a, s);
 }
@@ -777,11 +772,10 @@ AttendPlan attend_plan(int n_seqs, int hk, int group, int d, int dtype, int max_
   const int64_t pairs = (int64_t)n_seqs * hk;
   p.r_max = max_q * group;
   p.max_nb = (max_len + kBlk - 1) / kBlk;
-  const int cap = max_tiles(d, dtype == PI_F32);
-  p.nb = 1;
-  while (p.nb < cap && p.nb * 16 < p.r_max) p.nb *= 2;
-  p.many = p.r_max > most_rows_few(dtype == PI_F32);
-  const int wg_rows = p.many ? 16 * cap * kManyWaves : 16 * p.nb;
+  const bool f32 = dtype == PI_F32;
+  p.nb = p.r_max > 16 ? few_tiles(d) : 1;
+  p.many = p.r_max > most_rows_few(d, f32);
+  const int wg_rows = p.many ? 16 * many_tiles(d, f32) * kManyWaves : 16 * p.nb;
   p.tiles = (p.r_max + wg_rows - 1) / wg_rows;
   const int64_t wgs = pairs * p.tiles;
   int64_t splits = ((p.many ? 256 : 1024) + wgs - 1) / wgs;
