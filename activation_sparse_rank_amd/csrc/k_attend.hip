@@ -422,26 +422,23 @@ __global__ __launch_bounds__(kAtThreads, 2) void k_attend(AttendArgs a) {
     x.set_units(vs, rows.vref);
     // One set of registers for the codes: the next block's keys are on their
     // way from the end of the first product on, its values from the second's.
-    // (The last block is a step of its own: loads under a condition would be
-    // waited for as if they had not been issued.)
-    auto step = [&](int i, auto more) {
+    // (Past the last block they read page 0, which the caches hold: loads under a
+    // condition would be waited for as if they had not been issued.)
+    for (int i = 0; i < cnt; ++i) {
+      const int n = i + 1 < kWave ? i + 1 : i;
       rows.block(
           a, w, x, i, start + (base + i) * kAtWaves, kmin,
           [&](int mb, int kk, int f) {
             const u32x4 v = rk[mb * KK + kk];
             return f ? codes_f16(v.z, v.w) : codes_f16(v.x, v.y);
           },
-          [&] {
-            if constexpr (decltype(more)::value) load_k(i + 1);
-          },
+          [&] { load_k(n); },
           [&](int t) {
             const u32x4 v = rv[t / 2];
             return t % 2 ? codes_f16(v.z, v.w) : codes_f16(v.x, v.y);
           });
-      if constexpr (decltype(more)::value) load_v(i + 1);
-    };
-    for (int i = 0; i + 1 < cnt; ++i) step(i, std::true_type());
-    step(cnt - 1, std::false_type());
+      load_v(n);
+    }
   }
   raise_flag_if_any(a.flags, bad, PI_FLAG_KV_RANGE);
   rows.finish();
@@ -778,10 +775,14 @@ AttendPlan attend_plan(int n_seqs, int hk, int group, int d, int dtype, int max_
   const int wg_rows = p.many ? 16 * many_tiles(d, f32) * kManyWaves : 16 * p.nb;
   p.tiles = (p.r_max + wg_rows - 1) / wg_rows;
   const int64_t wgs = pairs * p.tiles;
-  int64_t splits = ((p.many ? 256 : 1024) + wgs - 1) / wgs;
+  // Splits as long as all workgroups run at once (one a CU of k_attend_many's,
+  // two of k_attend's): 8 x 32 pairs of 8192 tokens, D = 128, 98 us with four
+  // splits and 93 with two; 56 x 4 pairs of 4001 tokens in fp32 48 us with five, 42 with two.
+  int64_t splits = (p.many ? 256 : 512) / wgs;
   const int64_t most = (p.max_nb + 7) / 8;
   splits = splits < most ? splits : most;
-  p.splits = (int)(splits < kMaxSplits ? splits : kMaxSplits);
+  splits = splits < kMaxSplits ? splits : kMaxSplits;
+  p.splits = (int)(splits > 1 ? splits : 1);
   auto up256 = [](size_t v) { return (v + 255) & ~size_t(255); };
   size_t off = PI_WS_HEADER_BYTES;
   p.part = off;
