@@ -4,36 +4,46 @@
 // y = x * w / sqrt(mean(x^2) + eps); pair (a, b) -> scale * (a cos - b sin,
 // b cos + a sin).  Memory bound: every element is read and written once, and
 // what a token's heads share, its cosines and sines, is computed once per
-// workgroup into LDS (rot / 2 angles, reduced in 64 bits), while the first
-// heads' loads are in flight.  A workgroup owns one token; D / (16 bytes)
-// lanes hold a head, so a norm's sum is a butterfly inside a wave and a
-// half-layout element finds its partner by a second 16-byte load that the
-// first level cache answers.
+// workgroup into LDS (rot / 2 angles, reduced in 64 bits) while the first heads'
+// loads are in flight.  A workgroup owns one token; a few lanes hold a head, so a norm's
+// sum is a butterfly inside a wave.  In the half layout a lane takes 16 bytes
+// of the first half and the 16 bytes that they are paired with, so nothing is
+// read twice and nothing changes lanes.
 #include "attn_device.h"
 
 namespace pi {
 namespace {
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 1024;
 constexpr int kRopeMaxD = 256;
 
 // Workgroups of a call with few tokens split the heads, so that one token is
 // not one CU's work alone.
 constexpr int kRopeMinGroups = 512;
+constexpr int64_t kRopeFill = 256 * 2048;      // threads that the CUs hold
 
-// PART: 0 interleaved; 1 half layout, rot / 2 a multiple of the 16-byte
-// chunk; 2 half layout, partners at any offset (loaded one by one).
-template <typename T, int PART, bool NORM>
+// How a head is laid over lanes.
+enum : int {
+  kRopeInter,    // interleaved: a chunk of 16 bytes holds whole pairs
+  kRopePairs,    // half layout, rot / 2 a multiple of the chunk: a lane has both chunks of its pairs
+  kRopeAny       // half layout, partners at any offset: loaded one by one
+};
+
+template <typename T, int KIND, bool NORM>
 __global__ __launch_bounds__(kRopeThreads) void k_qk_rope(RopeArgs a, int group, int hsplit) {
   constexpr int V = Vec<T>::N;
+  constexpr bool kTwo = KIND == kRopePairs;
   __shared__ float2 cs[kRopeMaxD / 2];
   __shared__ float wn[NORM ? 2 * kRopeMaxD : 1];
   const int tok = blockIdx.x / hsplit, part = blockIdx.x % hsplit;
   const int half = a.rot / 2;
-  const int per = kRopeThreads / group;
+  const int per = blockDim.x / group;
   const int lane = threadIdx.x % group;
-  const int e0 = lane * V;
+  // This lane's chunk of each head; rotated pairs' second chunk is half later.
+  const int pairs = half / V;
+  const int e0 = kTwo && lane >= pairs ? a.rot + (lane - pairs) * V : lane * V;
   const bool in_head = e0 < a.d;
+  const bool two = kTwo && lane < pairs;
   const int n_heads = a.in[0].n + a.in[1].n;
   const int step = per * hsplit;
 
@@ -43,14 +53,13 @@ __global__ __launch_bounds__(kRopeThreads) void k_qk_rope(RopeArgs a, int group,
     return static_cast<T*>(x.p) + (int64_t)tok * x.ts + (int64_t)(i ? h - a.in[0].n : h) * x.hs;
   };
   // A chunk of the head and, in the half layout, its partners.
-  u32x4 x = {0, 0, 0, 0}, xp = {0, 0, 0, 0};
-  auto load = [&](int h) {
+  auto load = [&](int h, u32x4& x, u32x4& xp) {
     if (h >= n_heads || !in_head) return;
     const T* p = row(a.in, h);
-    x = ld16(p + e0);
-    if constexpr (PART == 1) {
-      if (e0 < a.rot) xp = ld16(p + (e0 < half ? e0 + half : e0 - half));
-    } else if constexpr (PART == 2) {
+    x = ld_nt(p + e0);
+    if constexpr (KIND == kRopePairs) {
+      if (two) xp = ld_nt(p + e0 + half);
+    } else if constexpr (KIND == kRopeAny) {
       if (e0 < a.rot) {
         float f[V];
 #pragma unroll
@@ -64,8 +73,9 @@ __global__ __launch_bounds__(kRopeThreads) void k_qk_rope(RopeArgs a, int group,
   };
 
   int h = part * per + threadIdx.x / group;
-  load(h);
-  for (int i = threadIdx.x; i < half; i += kRopeThreads) {
+  u32x4 x = {0, 0, 0, 0}, xp = {0, 0, 0, 0};
+  load(h, x, xp);
+  for (int i = threadIdx.x; i < half; i += blockDim.x) {
     double t = (double)a.pos[tok] * a.freqs[i];
     t -= rint(t);
     float s, c;
@@ -73,15 +83,25 @@ __global__ __launch_bounds__(kRopeThreads) void k_qk_rope(RopeArgs a, int group,
     cs[i] = float2{a.scale * c, a.scale * s};
   }
   if constexpr (NORM) {
-    for (int i = threadIdx.x; i < a.d; i += kRopeThreads) {
+    for (int i = threadIdx.x; i < a.d; i += blockDim.x) {
       wn[i] = a.w[0] ? a.w[0][i] : 1.f;
       wn[kRopeMaxD + i] = a.w[1] ? a.w[1][i] : 1.f;
     }
   }
   __syncthreads();
+  // The same for every head of this lane.
+  float2 t[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int e = e0 + i;
+    t[i] = float2{1.f, 0.f};
+    if (e < a.rot) t[i] = cs[KIND == kRopeInter ? e / 2 : (e < half ? e : e - half)];
+  }
 
   for (; h - (int)(threadIdx.x / group) < n_heads; h += step) {
     const bool mine = h < n_heads && in_head;
+    u32x4 nx = {0, 0, 0, 0}, nxp = {0, 0, 0, 0};
+    load(h + step, nx, nxp);
     float y[V], yp[V];
     Vec<T>::unpack(x, y);
     Vec<T>::unpack(xp, yp);
@@ -90,6 +110,10 @@ __global__ __launch_bounds__(kRopeThreads) void k_qk_rope(RopeArgs a, int group,
       if (mine) {
 #pragma unroll
         for (int i = 0; i < V; ++i) ss = __builtin_fmaf(y[i], y[i], ss);
+        if (two) {
+#pragma unroll
+          for (int i = 0; i < V; ++i) ss = __builtin_fmaf(yp[i], yp[i], ss);
+        }
       }
       for (int m = group / 2; m >= 1; m >>= 1) ss += __shfl_xor(ss, m, kWave);
       const int k = h >= a.in[0].n;
@@ -98,64 +122,82 @@ __global__ __launch_bounds__(kRopeThreads) void k_qk_rope(RopeArgs a, int group,
         const float* w = wn + k * kRopeMaxD;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-          y[i] = y[i] * r * w[e0 + i];
-          if constexpr (PART > 0) {
-            const int e = e0 + i;
+          const int e = e0 + i;
+          y[i] = y[i] * r * w[e];
+          if constexpr (KIND != kRopeInter)
             if (e < a.rot) yp[i] = yp[i] * r * w[e < half ? e + half : e - half];
-          }
         }
       }
     }
     if (mine) {
+      T* p = row(a.out, h) + e0;
       float o[V];
-      if constexpr (PART == 0) {
+      if constexpr (KIND == kRopeInter) {
 #pragma unroll
         for (int i = 0; i < V; i += 2) {
-          o[i] = y[i], o[i + 1] = y[i + 1];
-          if (e0 + i < a.rot) {
-            const float2 t = cs[(e0 + i) / 2];
-            o[i] = __builtin_fmaf(y[i], t.x, -(y[i + 1] * t.y));
-            o[i + 1] = __builtin_fmaf(y[i + 1], t.x, y[i] * t.y);
+          // (1, 0) past the rotated elements: y * 1 - z * 0 must not make a NaN of an infinite z
+          const bool in = e0 + i < a.rot;
+          o[i] = in ? __builtin_fmaf(y[i], t[i].x, -(y[i + 1] * t[i].y)) : y[i];
+          o[i + 1] = in ? __builtin_fmaf(y[i + 1], t[i].x, y[i] * t[i].y) : y[i + 1];
+        }
+        *reinterpret_cast<u32x4*>(p) = Vec<T>::pack(o);
+      } else if constexpr (KIND == kRopePairs) {
+        if (two) {
+          float q[V];
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            o[i] = __builtin_fmaf(y[i], t[i].x, -(yp[i] * t[i].y));
+            q[i] = __builtin_fmaf(yp[i], t[i].x, y[i] * t[i].y);
           }
+          *reinterpret_cast<u32x4*>(p) = Vec<T>::pack(o);
+          *reinterpret_cast<u32x4*>(p + half) = Vec<T>::pack(q);
+        } else {
+          *reinterpret_cast<u32x4*>(p) = Vec<T>::pack(y);
         }
       } else {
 #pragma unroll
         for (int i = 0; i < V; ++i) {
           const int e = e0 + i;
-          o[i] = y[i];
-          if (e < a.rot) {
-            const float2 t = cs[e < half ? e : e - half];
-            o[i] = __builtin_fmaf(y[i], t.x, e < half ? -(yp[i] * t.y) : yp[i] * t.y);
-          }
+          const float s = e < half ? -(yp[i] * t[i].y) : yp[i] * t[i].y;
+          o[i] = e < a.rot ? __builtin_fmaf(y[i], t[i].x, s) : y[i];
         }
+        *reinterpret_cast<u32x4*>(p) = Vec<T>::pack(o);
       }
-      *reinterpret_cast<u32x4*>(row(a.out, h) + e0) = Vec<T>::pack(o);
     }
-    load(h + step);
+    x = nx, xp = nxp;
   }
 }
 
-template <typename T, int PART>
-hipError_t rope_part(const RopeArgs& a, int group, int hsplit, hipStream_t s) {
+template <typename T, int KIND>
+hipError_t rope_kind(const RopeArgs& a, hipStream_t s) {
+  constexpr int V = Vec<T>::N;
+  const int lanes = KIND == kRopePairs ? a.rot / 2 / V + (a.d - a.rot) / V : a.d / V;
+  int group = 1;                                      // a power of two, so that a head stays in a wave
+  while (group < lanes) group *= 2;
+  const int n_heads = a.in[0].n + a.in[1].n;
+  // A token's heads in passes of one size.  Threads by what fills the card, at
+  // least 256: 4096 tokens of 72 fp16 heads 31.9 us with 256 (three passes) and 46.7
+  // with 1024 (one); 777 tokens of 112 fp32 heads 23.1 and 18.9.  Very few
+  // tokens: a pass to a workgroup of few threads.
+  int most = 256;
+  while (most < kRopeThreads && (int64_t)a.n_tok * most < kRopeFill) most *= 2;
+  while (most > 256 && (int64_t)a.n_tok * (((int64_t)n_heads * group + most - 1) / most) < kRopeMinGroups) most /= 2;
+  const int passes = (int)(((int64_t)n_heads * group + most - 1) / most);
+  const int threads = (int)(((int64_t)n_heads * group + passes - 1) / passes + kWave - 1) / kWave * kWave;
+  int hsplit = (kRopeMinGroups + a.n_tok - 1) / a.n_tok;
+  hsplit = hsplit < passes ? hsplit : passes;
   const dim3 grid((unsigned)a.n_tok * hsplit);
   if (a.w[0] || a.w[1])
-    k_qk_rope<T, PART, true><<<grid, kRopeThreads, 0, s>>>(a, group, hsplit);
+    k_qk_rope<T, KIND, true><<<grid, threads, 0, s>>>(a, group, hsplit);
   else
-    k_qk_rope<T, PART, false><<<grid, kRopeThreads, 0, s>>>(a, group, hsplit);
+    k_qk_rope<T, KIND, false><<<grid, threads, 0, s>>>(a, group, hsplit);
   return hipGetLastError();
 }
 
 template <typename T>
 hipError_t rope_type(const RopeArgs& a, hipStream_t s) {
-  constexpr int V = Vec<T>::N;
-  int group = 1;
-  while (group * V < a.d) group *= 2;
-  const int per = kRopeThreads / group;
-  const int passes = (a.in[0].n + a.in[1].n + per - 1) / per;
-  int hsplit = (kRopeMinGroups + a.n_tok - 1) / a.n_tok;
-  hsplit = hsplit < passes ? hsplit : passes;
-  if (a.layout == PI_ROPE_INTERLEAVED) return rope_part<T, 0>(a, group, hsplit, s);
-  return (a.rot / 2) % V ? rope_part<T, 2>(a, group, hsplit, s) : rope_part<T, 1>(a, group, hsplit, s);
+  if (a.layout == PI_ROPE_INTERLEAVED) return rope_kind<T, kRopeInter>(a, s);
+  return (a.rot / 2) % Vec<T>::N ? rope_kind<T, kRopeAny>(a, s) : rope_kind<T, kRopePairs>(a, s);
 }
 
 }  // namespace
