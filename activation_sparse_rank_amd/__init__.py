@@ -29,6 +29,7 @@ from .api import (  # noqa: F401
     sparse_ffn,
     workspace_bytes,
 )
+from . import attention  # noqa: F401
 from .attention import (  # noqa: F401
     KVCache,
     Rope,

@@ -5,7 +5,9 @@ accumulated attention weight (``kv_evict``).
 
 As in ``api``, each function checks what the C ABI cannot see (devices,
 types, shapes, strides) and forwards pointers and the current HIP stream;
-include/pi.h says what each call computes.  Token rows are
+include/pi.h says what each call computes.  The checks are native
+(csrc/bind_attn.cpp): these calls run for a few microseconds each, once or more per
+layer and token.  Token rows are
 [n_tok, n_heads, head_dim] tensors whose last dimension is contiguous, so
 views into a fused projection's output are taken as they are.  Calls run on
 the tensors' device.
@@ -14,77 +16,37 @@ the tensors' device.
 from __future__ import annotations
 
 import ctypes
+import importlib
 import math
 
 import torch
 
 from . import _lib as L
-from .api import _DTYPES, _check, _dev, _ptr
+from .api import _DTYPES, PiError, _dev, _ptr
 
 _LAYOUTS = {"half": L.PI_ROPE_HALF, "interleaved": L.PI_ROPE_INTERLEAVED}
 
-# A decode step's calls take a few microseconds on the GPU, less than careless
-# checks take here: each check below reads a tensor's attributes once, and
-# says what is wrong only after something is (8.2 -> 5.5 us for a
-# one-token qk_rope, of which 2.5 are the launch).
-_Tensor = torch.Tensor
-_int32 = torch.int32
-# The current stream's handle without an object around it (1.1 -> 0.1 us).
-_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+_native = None
 
 
-def _stream(stream, dev: int):
-    """The raw handle of stream, or of the current stream of device dev."""
-    if stream is None:
-        return _current_stream(dev)
-    return stream if isinstance(stream, int) else stream.cuda_stream
+def load_native():
+    """Load the native module that checks the tensors and calls libpi (bind_attn.cpp); raise if it has not been built."""
+    global _native
+    if _native is None:
+        lib = L.load()
+        try:
+            native = importlib.import_module("._attn", __package__)
+        except ImportError as e:
+            raise ImportError("the attention side's binding is not built; run `python -m "
+                              f"activation_sparse_rank_amd.build` ({e})") from e
+        native.use_library(lib._handle)
+        _native = native
+    return _native
 
 
-def _rows(t, name, heads, d, dtype, dev):
-    """Checks token rows; returns (pointer, token stride, head stride, tokens)."""
-    if isinstance(t, _Tensor) and t.dtype is dtype and t.get_device() == dev:
-        shape = t.shape
-        if len(shape) == 3:
-            n, h, e = shape
-            ts, hs, es = t.stride()
-            if h == heads and e == d and es == 1:
-                return t.data_ptr(), ts, hs, n
-    _bad_rows(t, name, heads, d, dtype, dev)
-
-
-def _bad_rows(t, name, heads, d, dtype, dev):
-    if not isinstance(t, _Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} must live in GPU memory, on the same device as the rest")
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d:
-        raise ValueError(f"{name} must be [n_tok, {heads}, {d}]")
-    raise ValueError(f"{name}: the elements of a head must be contiguous")
-
-
-def _i32(t, name, n, dev):
-    """Checks a contiguous int32 vector of n entries on device dev; returns its pointer."""
-    if (isinstance(t, _Tensor) and t.dtype is _int32 and t.get_device() == dev and t.shape == (n,)
-            and t.is_contiguous()):
-        return t.data_ptr()
-    if not isinstance(t, _Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != _int32 or t.shape != (n,) or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous int32 [{n}]")
-    raise ValueError(f"{name} must live in GPU memory, on the same device as the rest")
-
-
-def _same(t, name, like, dtype, dev):
-    """Checks a contiguous tensor of dtype with the shape ``like`` on device dev; returns its pointer."""
-    if isinstance(t, _Tensor) and t.dtype is dtype and t.get_device() == dev and t.shape == like and t.is_contiguous():
-        return t.data_ptr()
-    _dev(t, name)
-    if t.dtype != dtype or t.shape != like:
-        raise ValueError(f"{name} must be {dtype} {list(like)}")
-    raise ValueError(f"{name} must be on the same device as the rest")
+def _handle(stream):
+    """The raw handle of a stream; None stays None (the tensors' device's current stream)."""
+    return stream if stream is None or isinstance(stream, int) else stream.cuda_stream
 
 
 class Rope:
@@ -123,30 +85,17 @@ class Rope:
         self.head_dim, self.rot, self.layout, self.scale, self.eps = head_dim, rot, layout, scale, eps
         self._dev = freqs.get_device()
         self.desc = L.PiRope(head_dim, rot, _LAYOUTS[layout], scale, eps, freqs.data_ptr(), _ptr(q_norm), _ptr(k_norm))
-        self._ref = ctypes.byref(self.desc)
+        self._addr = ctypes.addressof(self.desc)
 
 
 def qk_rope(rope: Rope, q, k, pos, q_out=None, k_out=None, stream=None):
     """Norms (where rope has weights) and rotation of queries and keys at the
     positions ``pos`` (int32 [n_tok]), in one pass (pi_qk_rope).  Without
     ``q_out`` / ``k_out`` the inputs are rotated in place.  Returns (q_out, k_out)."""
-    if not (isinstance(q, _Tensor) and isinstance(k, _Tensor) and q.dim() == 3 and k.dim() == 3):
-        raise TypeError("q and k must be tensors [n_tok, heads, head_dim]")
-    dev, dt, d = rope._dev, q.dtype, rope.head_dim
-    if dt not in _DTYPES:
-        raise TypeError("q must be float16 or float32")
-    h, hk = q.shape[1], k.shape[1]
     q_out, k_out = q if q_out is None else q_out, k if k_out is None else k_out
-    qp, qt, qh, n = _rows(q, "q", h, d, dt, dev)
-    kp, kt, kh, nk = _rows(k, "k", hk, d, dt, dev)
-    qo, qot, qoh, nqo = _rows(q_out, "q_out", h, d, dt, dev)
-    ko, kot, koh, nko = _rows(k_out, "k_out", hk, d, dt, dev)
-    if not n == nk == nqo == nko:
-        raise ValueError("q, k and their outputs must have the same tokens")
-    if n == 0:
-        return q_out, k_out
-    _check(L.load().pi_qk_rope(rope._ref, qp, qt, qh, h, kp, kt, kh, hk, _i32(pos, "pos", n, dev), n, _DTYPES[dt],
-                               qo, qot, qoh, ko, kot, koh, _stream(stream, dev)), "pi_qk_rope")
+    st = (_native or load_native()).qk_rope(rope._addr, rope._dev, q, k, pos, q_out, k_out, _handle(stream))
+    if st:
+        raise PiError(st, "pi_qk_rope")
     return q_out, k_out
 
 
@@ -187,7 +136,7 @@ class KVCache:
         self._dev = pages.get_device()
         self.desc = L.PiKVCache(s, h, d, self.max_blocks, pages.shape[0], _DTYPES[open.dtype], pages.data_ptr(),
                                 scales.data_ptr(), open.data_ptr(), table.data_ptr(), _ptr(score))
-        self._ref = ctypes.byref(self.desc)
+        self._ref, self._addr = ctypes.byref(self.desc), ctypes.addressof(self.desc)
 
 
 def kv_append(cache: KVCache, k, v, lens, q_start=None, max_new=None, stream=None):
@@ -196,49 +145,21 @@ def kv_append(cache: KVCache, k, v, lens, q_start=None, max_new=None, stream=Non
     [n_seqs + 1]) gives each sequence's rows, at most ``max_new`` of them
     (default: all rows of k); without it every sequence has max_new rows, one after the other
     (default: n_tok / n_seqs)."""
-    h, d, dt, dev = cache.n_kv_heads, cache.head_dim, cache.dtype, cache._dev
-    kp, kt, kh, n = _rows(k, "k", h, d, dt, dev)
-    vp, vt, vh, nv = _rows(v, "v", h, d, dt, dev)
-    if n != nv:
-        raise ValueError("k and v must have the same tokens")
-    lp, qp, max_new = _bounds(cache, lens, q_start, max_new, n, dev)
-    if n == 0:
-        return
-    _check(L.load().pi_kv_append(cache._ref, kp, kt, kh, vp, vt, vh, n, lp, qp, max_new, _stream(stream, dev)),
-           "pi_kv_append")
+    st = (_native or load_native()).kv_append(cache._addr, cache._dev, k, v, lens, q_start, max_new, _handle(stream))
+    if st:
+        raise PiError(st, "pi_kv_append")
 
 
 def kv_read(cache: KVCache, lens, k_out, v_out, q_start=None, max_new=None, stream=None):
     """The values that the cache holds for the last rows of each sequence
     (pi_kv_read); lens, q_start and max_new as for kv_append."""
-    h, d, dt, dev = cache.n_kv_heads, cache.head_dim, cache.dtype, cache._dev
-    kp, kt, kh, n = _rows(k_out, "k_out", h, d, dt, dev)
-    vp, vt, vh, nv = _rows(v_out, "v_out", h, d, dt, dev)
-    if n != nv:
-        raise ValueError("k_out and v_out must have the same tokens")
-    lp, qp, max_new = _bounds(cache, lens, q_start, max_new, n, dev)
-    if n == 0:
-        return
-    _check(L.load().pi_kv_read(cache._ref, lp, qp, max_new, kp, kt, kh, vp, vt, vh, n, _stream(stream, dev)),
-           "pi_kv_read")
-
-
-def _bounds(cache, lens, q_start, max_q, n, dev):
-    """Pointers of lens and q_start, and the bound on a sequence's rows."""
-    s = cache.n_seqs
-    lp = _i32(lens, "lens", s, dev)
-    if q_start is None:
-        if max_q is None:
-            max_q = n // s
-        if n != s * max_q:
-            raise ValueError("without q_start there must be n_seqs * max rows")
-        return lp, None, max_q
-    return lp, _i32(q_start, "q_start", s + 1, dev), n if max_q is None else max_q
+    st = (_native or load_native()).kv_read(cache._addr, cache._dev, k_out, v_out, lens, q_start, max_new, _handle(stream))
+    if st:
+        raise PiError(st, "pi_kv_read")
 
 
 def attend_workspace_bytes(cache: KVCache, n_heads: int, max_q: int, max_len=None, add_score: bool = False) -> int:
     """Bytes of workspace attend needs for these bounds (pi_attend_workspace_bytes)."""
-    from .api import PiError
     if max_len is None:
         max_len = cache.max_blocks * L.PI_KV_BLOCK
     n = L.load().pi_attend_workspace_bytes(cache._ref, int(n_heads), int(max_q), int(max_len), int(add_score))
@@ -267,39 +188,31 @@ def attend(cache: KVCache, q, lens, out, q_start=None, max_q=None, max_len=None,
     weights of each block to cache.score.  ``ws`` from alloc_attend_workspace
     with the same bounds (one is allocated where it is None)."""
     d, dt, dev = cache.head_dim, cache.dtype, cache._dev
-    if not (isinstance(q, _Tensor) and q.dim() == 3):
-        raise TypeError("q must be a tensor [n_tok, n_heads, head_dim]")
-    h = q.shape[1]
-    qp, qt, qh, n = _rows(q, "q", h, d, dt, dev)
-    op, ot, oh, no = _rows(out, "out", h, d, dt, dev)
-    if n != no:
-        raise ValueError("q and out must have the same tokens")
-    lp, sp, max_q = _bounds(cache, lens, q_start, max_q, n, dev)
-    if n == 0:
-        return
     if max_len is None:
         max_len = cache.max_blocks * L.PI_KV_BLOCK
-    if add_score and cache.score is None:
-        raise ValueError("add_score needs a cache with a score")
     if ws is None:
-        ws = _temp_attend_workspace(cache, h, max_q, max_len, add_score, stream)
-    elif ws.dtype != torch.uint8 or not ws.is_contiguous() or ws.get_device() != dev:
-        raise ValueError("ws must be contiguous uint8 on the cache's device")
-    _check(L.load().pi_attend(cache._ref, qp, qt, qh, h, n, lp, sp, max_q, max_len,
-                              d ** -0.5 if scale is None else scale, bool(add_score), op, ot, oh, ws.data_ptr(),
-                              ws.numel(), _stream(stream, dev)), "pi_attend")
+        ws = _temp_attend_workspace(cache, q, max_q, max_len, add_score, q_start, stream)
+    st = (_native or load_native()).attend(cache._addr, cache._dev, q, lens, out, q_start, max_q, max_len,
+                                     cache.head_dim ** -0.5 if scale is None else scale, add_score, ws,
+                                     _handle(stream))
+    if st:
+        raise PiError(st, "pi_attend")
 
 
-def _temp_attend_workspace(cache, h, max_q, max_len, add_score, stream):
+def _temp_attend_workspace(cache, q, max_q, max_len, add_score, q_start, stream):
     """A workspace for one call, allocated on the call's stream, so that its
     memory is handed out again only in that stream's order."""
+    if not (isinstance(q, torch.Tensor) and q.dim() == 3):
+        raise TypeError("q must be a tensor [n_tok, n_heads, head_dim]")
+    if max_q is None:
+        max_q = q.shape[0] if q_start is not None else q.shape[0] // cache.n_seqs
     if stream is None:
-        return alloc_attend_workspace(cache, h, max_q, max_len, add_score)
+        return alloc_attend_workspace(cache, q.shape[1], max(1, max_q), max_len, add_score)
     s = stream
     if not isinstance(s, torch.cuda.Stream):
         s = torch.cuda.ExternalStream(int(stream), device=cache.pages.device)
     with torch.cuda.stream(s):
-        return alloc_attend_workspace(cache, h, max_q, max_len, add_score)
+        return alloc_attend_workspace(cache, q.shape[1], max(1, max_q), max_len, add_score)
 
 
 def kv_evict(table, score, lens, keep: int, recent: int, lens_out, table_out=None, score_out=None, stream=None):
@@ -308,19 +221,11 @@ def kv_evict(table, score, lens, keep: int, recent: int, lens_out, table_out=Non
     ``recent`` and the heaviest others; the pages that leave follow them in the
     table.  Without ``table_out`` and ``score_out`` table and score are
     rewritten in place; ``lens_out`` (int32 [n_seqs]) is never ``lens``."""
-    if not isinstance(table, _Tensor) or table.dtype is not _int32 or table.dim() != 3:
-        raise ValueError("table must be an int32 tensor [n_seqs, n_kv_heads, max_blocks]")
-    shape, dev = table.shape, table.get_device()
-    if dev < 0:
-        raise ValueError("table must live in GPU memory")
-    tp, sp = _same(table, "table", shape, _int32, dev), _same(score, "score", shape, torch.float32, dev)
     if (table_out is None) != (score_out is None):
         raise ValueError("table_out and score_out go together")
     if table_out is None:
-        to, so = tp, sp
-    else:
-        to = _same(table_out, "table_out", shape, _int32, dev)
-        so = _same(score_out, "score_out", shape, torch.float32, dev)
-    s, h, n = shape
-    _check(L.load().pi_kv_evict(tp, sp, _i32(lens, "lens", s, dev), s, h, n, keep, recent, to, so,
-                                _i32(lens_out, "lens_out", s, dev), _stream(stream, dev)), "pi_kv_evict")
+        table_out, score_out = table, score
+    st = (_native or load_native()).kv_evict(table, score, lens, keep, recent, lens_out, table_out, score_out,
+                                       _handle(stream))
+    if st:
+        raise PiError(st, "pi_kv_evict")
