@@ -725,22 +725,21 @@ constexpr int many_tiles(int d, bool f32) { return d == 128 && f32 ? 1 : 2; }
 
 // k_attend up to so many rows, k_attend_many beyond.  Measured on one card: fp16, D =
 // 128, 4 sequences of 8192 tokens, 32 rows 45.5 us here (two tiles a wave) and
-// 36.7 there; D = 64, 32 rows over 8000 tokens 12.6 and 15.7 us, 64 rows 25.9
-// and 17.0; fp32 (twice the products either way), D = 64, 128 rows 16.5 and
-// 20.1, 256 rows 27.6 and 27.8, 512 rows 34.4 and 31.1.
+// 27.3 there; D = 64, 32 rows over 8000 tokens 12.2 and 15.7 us, 64 rows 25.9
+// and 14.7; fp32 (twice the products either way), D = 64, 128 rows 16.6 and
+// 20.1, 256 rows 17.7 and 27.8, 512 rows 34.4 and 30.5.
 constexpr int most_rows_few(int d, bool f32) { return f32 ? 256 : 16 * few_tiles(d); }
 
-// Launches one of the two kernels (NB 0: k_attend_many) and the join.
-template <typename T, int D, int NB>
+// Launches one of the two kernels and the join.
+template <typename T, int D, int NB, bool MANY>
 hipError_t attend_run(const AttendArgs& a, hipStream_t s) {
   const int pairs = a.n_seqs * a.hk;
   const dim3 grid((unsigned)pairs * a.tiles * a.splits);
-  if constexpr (NB == 0) {
+  if constexpr (MANY) {
     // Two groups where the rows' registers leave room for four waves a SIMD.
     constexpr int G = D == 64 && sizeof(T) == 2 ? 2 : 1;
-    constexpr int M = many_tiles(D, sizeof(T) == 4);
-    if (a.score) k_attend_many<T, D, M, true, 1><<<grid, kManyThreads, 0, s>>>(a);
-    else k_attend_many<T, D, M, false, G><<<grid, G * kManyThreads, 0, s>>>(a);
+    if (a.score) k_attend_many<T, D, NB, true, 1><<<grid, kManyThreads, 0, s>>>(a);
+    else k_attend_many<T, D, NB, false, G><<<grid, G * kManyThreads, 0, s>>>(a);
   } else {
     if (a.score) k_attend<T, D, NB, true><<<grid, kAtThreads, 0, s>>>(a);
     else k_attend<T, D, NB, false><<<grid, kAtThreads, 0, s>>>(a);
@@ -756,10 +755,16 @@ hipError_t attend_run(const AttendArgs& a, hipStream_t s) {
 
 template <typename T, int D>
 hipError_t attend_nb(const AttendArgs& a, const AttendPlan& p, hipStream_t s) {
-  if (p.many) return attend_run<T, D, 0>(a, s);
+  constexpr bool f32 = sizeof(T) == 4;
+  if (p.many) {
+    // (fp32 rows come here in such numbers that they fill the wider tiles)
+    if constexpr (!f32)
+      if (p.nb == 1) return attend_run<T, D, 1, true>(a, s);
+    return attend_run<T, D, many_tiles(D, f32), true>(a, s);
+  }
   if constexpr (few_tiles(D) == 2)
-    if (p.nb == 2) return attend_run<T, D, 2>(a, s);
-  return attend_run<T, D, 1>(a, s);
+    if (p.nb == 2) return attend_run<T, D, 2, false>(a, s);
+  return attend_run<T, D, 1, false>(a, s);
 }
 
 }  // namespace
@@ -770,9 +775,11 @@ AttendPlan attend_plan(int n_seqs, int hk, int group, int d, int dtype, int max_
   p.r_max = max_q * group;
   p.max_nb = (max_len + kBlk - 1) / kBlk;
   const bool f32 = dtype == PI_F32;
-  p.nb = p.r_max > 16 ? few_tiles(d) : 1;
   p.many = p.r_max > most_rows_few(d, f32);
-  const int wg_rows = p.many ? 16 * many_tiles(d, f32) * kManyWaves : 16 * p.nb;
+  // One tile a wave while that is enough: more waves share the rows.
+  const int narrow = p.many ? 16 * kManyWaves : 16;
+  p.nb = p.r_max <= narrow ? 1 : (p.many ? many_tiles(d, f32) : few_tiles(d));
+  const int wg_rows = narrow * p.nb;
   p.tiles = (p.r_max + wg_rows - 1) / wg_rows;
   const int64_t wgs = pairs * p.tiles;
   // Splits as long as all workgroups run at once (one a CU of k_attend_many's,
