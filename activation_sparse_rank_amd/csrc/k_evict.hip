@@ -43,6 +43,18 @@ __device__ __forceinline__ unsigned wave_scan(unsigned x) {
   return (unsigned)v;
 }
 
+// The largest of the lanes' values, in lane 63 (the same steps).
+__device__ __forceinline__ unsigned wave_max(unsigned v) {
+  auto step = [&](unsigned x) { v = v > x ? v : x; };
+  step((unsigned)__builtin_amdgcn_update_dpp(0, (int)v, 0x111, 0xf, 0xf, false));
+  step((unsigned)__builtin_amdgcn_update_dpp(0, (int)v, 0x112, 0xf, 0xf, false));
+  step((unsigned)__builtin_amdgcn_update_dpp(0, (int)v, 0x114, 0xf, 0xf, false));
+  step((unsigned)__builtin_amdgcn_update_dpp(0, (int)v, 0x118, 0xf, 0xf, false));
+  step((unsigned)__builtin_amdgcn_update_dpp(0, (int)v, 0x142, 0xa, 0xf, false));
+  step((unsigned)__builtin_amdgcn_update_dpp(0, (int)v, 0x143, 0xc, 0xf, false));
+  return v;
+}
+
 // How many of keys[0 .. n) go before the key k of number i: larger, or equal
 // with a lower number.  The wave's lanes have the numbers base .. base + 63 and
 // their keys (0 past n); n is a multiple of 4.
@@ -166,17 +178,15 @@ __global__ __launch_bounds__(kEvThreads) void k_kv_evict(EvictArgs a) {
 #pragma unroll R
     for (int c = 0; c < chunks; ++c) {
       const int i = c * kEvThreads + tid;
+      if (c * kEvThreads >= old) break;
       if (i < old) {
         const unsigned k = key_at(c, i);
         least = least < k ? least : k, most = most > k ? most : k;
       }
     }
-#pragma unroll
-    for (int m = 32; m >= 1; m >>= 1) {
-      const unsigned x = (unsigned)__shfl_xor((int)least, m, kWave), y = (unsigned)__shfl_xor((int)most, m, kWave);
-      least = least < x ? least : x, most = most > y ? most : y;
-    }
-    if (lane_id() == 0) ends[wave_id()] = uint2{least, most};
+    // least as the complement of the largest complement
+    const uint2 e = {~wave_max(~least), wave_max(most)};
+    if (lane_id() == kWave - 1) ends[wave_id()] = e;
     for (int i = tid; i < kBins; i += kEvThreads) hist[i] = 0;
     if (tid < kRankMax) ckey[tid] = 0;
     if (tid == 0) found = 0;
@@ -195,6 +205,7 @@ __global__ __launch_bounds__(kEvThreads) void k_kv_evict(EvictArgs a) {
 #pragma unroll R
       for (int c = 0; c < chunks; ++c) {
         const int i = c * kEvThreads + tid;
+        if (c * kEvThreads >= old) break;
         if (i < old) {
           const unsigned k = key_at(c, i);
           if (inside(k)) atomicAdd(&hist[(k - base) >> shift], 1u);
@@ -225,6 +236,7 @@ __global__ __launch_bounds__(kEvThreads) void k_kv_evict(EvictArgs a) {
 #pragma unroll R
         for (int c = 0; c < chunks; ++c) {
           const int i = c * kEvThreads + tid;
+          if (c * kEvThreads >= old) break;
           if (i < old) {
             const unsigned k = key_at(c, i);
             if (inside(k)) {
@@ -297,7 +309,7 @@ __global__ __launch_bounds__(kEvThreads) void k_kv_evict(EvictArgs a) {
 #pragma unroll
     for (int c = 0; c < R; ++c) {
       const int i = c * kEvThreads + tid;
-      b[c] = __ballot(i < old && stays(i, sc[c]));
+      b[c] = c * kEvThreads < old ? __ballot(i < old && stays(i, sc[c])) : 0;
       if (lane_id() == 0) kept[c * kEvWaves + wave_id()] = __popcll(b[c]);
     }
     __syncthreads();                                  // also: every slot has been read
@@ -314,6 +326,7 @@ __global__ __launch_bounds__(kEvThreads) void k_kv_evict(EvictArgs a) {
 #pragma unroll
     for (int c = 0; c < R; ++c) {
       const int i = c * kEvThreads + tid, e = c * kEvWaves + wave_id();
+      if (c * kEvThreads >= n) break;
       int pre = 0;
 #pragma unroll
       for (int k = 0; k < PER; ++k)

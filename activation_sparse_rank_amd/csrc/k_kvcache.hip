@@ -11,7 +11,9 @@
 namespace pi {
 namespace {
 
-constexpr int kKvThreads = 256;
+// Threads of a workgroup: one for each 16 bytes of a page's half.  (128 for D =
+// 64: a prompt's 2080 workgroups run in one round, where 256 threads each left a second one.)
+constexpr int kv_threads(int d) { return 2 * d; }
 
 // Blocks that a call of max_new rows can touch in one sequence.
 int touched_blocks(int max_new) { return (int)(((long long)max_new + 2 * kBlk - 2) / kBlk); }
@@ -31,11 +33,17 @@ struct Unit {
   }
 };
 
-// 128 + rint(127 x / amax).  The fp32 quotient decides but for values within
-// 1e-3 of the middle of two codes, where 254 |x| and (2 k + 1) amax are
-// compared exactly in 64 bits (a tie goes to the even code).  x and amax are
-// finite, amax > 0; inv = 127 / amax.
-__device__ __forceinline__ unsigned code_of(float x, float amax, float inv) {
+// code - 128 = rint(127 x / amax) as a float, by the fp32 quotient; close: it
+// lies within 1e-3 of the middle of two codes, where exact_code decides.  x and
+// amax are finite, amax > 0; inv = 127 / amax.
+__device__ __forceinline__ float quick_code(float x, float inv, bool& close) {
+  const float r = x * inv, q = rintf(r);
+  close |= __builtin_fabsf(r - q) > 0.499f;
+  return q;
+}
+
+// 254 |x| against the middle (2 k + 1) amax, both exact in 64 bits; a tie goes to the even code.
+__device__ __forceinline__ float exact_code(float x, float amax, float inv) {
   const float r = __builtin_fabsf(x) * inv;
   float q = rintf(r);
   if (__builtin_fabsf(r - q) > 0.499f) {
@@ -44,13 +52,12 @@ __device__ __forceinline__ unsigned code_of(float x, float amax, float inv) {
     const bool odd = ((int)k & 1) != 0;
     q = n > mid || (n == mid && odd) ? k + 1.f : k;
   }
-  const int c = (int)q;
-  return (unsigned)(128 + (x < 0.f ? -c : c));
+  return x < 0.f ? -q : q;
 }
 
 template <typename T, int D>
-__global__ __launch_bounds__(kKvThreads) void k_kv_append(CacheArgs a, int count) {
-  constexpr int V = Vec<T>::N, CH = D / V, N = kBlk * CH / kKvThreads;
+__global__ __launch_bounds__(kv_threads(D)) void k_kv_append(CacheArgs a, int count) {
+  constexpr int kKvThreads = kv_threads(D), V = Vec<T>::N, CH = D / V, N = kBlk * CH / kKvThreads;
   constexpr int kRow = D + 16;                      // bytes of an LDS row (16 more: no bank conflicts down a column)
   __shared__ alignas(16) uint8_t codes[kBlk * kRow];
   __shared__ unsigned red[kKvThreads / kWave];
@@ -101,10 +108,19 @@ __global__ __launch_bounds__(kKvThreads) void k_kv_append(CacheArgs a, int count
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     const int id = i * kKvThreads + threadIdx.x, t = id / CH, e = id % CH * V;
+    float q[V];
+    bool close = false;
+#pragma unroll
+    for (int k = 0; k < V; ++k) q[k] = quick_code(x[i][k] * up, inv, close);
+    // (one branch for all the elements: some lane's is close in one chunk of ten)
+    if (close) {
+#pragma unroll
+      for (int k = 0; k < V; ++k) q[k] = exact_code(x[i][k] * up, amax * up, inv);
+    }
     unsigned w[V / 4];
 #pragma unroll
     for (int k = 0; k < V; ++k) {
-      const unsigned c = finite && top != 0 ? code_of(x[i][k] * up, amax * up, inv) : 128u;
+      const unsigned c = finite && top != 0 ? (unsigned)(128 + (int)q[k]) : 128u;
       w[k / 4] = k % 4 ? w[k / 4] | c << 8 * (k % 4) : c;
     }
 #pragma unroll
@@ -113,23 +129,21 @@ __global__ __launch_bounds__(kKvThreads) void k_kv_append(CacheArgs a, int count
   __syncthreads();
   if ((unsigned)page < (unsigned)a.n_pages) {
     const int u = threadIdx.x;
-    if (u < 2 * D) {
-      u32x4 out;
-      int t, e;
-      if (half == 0) {
-        Unit<D>::key(u, t, e);
-        out = *reinterpret_cast<const u32x4*>(codes + t * kRow + e);
-      } else {
-        unsigned w[4] = {0, 0, 0, 0};
+    u32x4 out;
+    int t, e;
+    if (half == 0) {
+      Unit<D>::key(u, t, e);
+      out = *reinterpret_cast<const u32x4*>(codes + t * kRow + e);
+    } else {
+      unsigned w[4] = {0, 0, 0, 0};
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          Unit<D>::value(u, k, t, e);
-          w[k / 4] |= (unsigned)codes[t * kRow + e] << 8 * (k % 4);
-        }
-        out = u32x4{w[0], w[1], w[2], w[3]};
+      for (int k = 0; k < 16; ++k) {
+        Unit<D>::value(u, k, t, e);
+        w[k / 4] |= (unsigned)codes[t * kRow + e] << 8 * (k % 4);
       }
-      *reinterpret_cast<u32x4*>(a.pages + ((int64_t)page * 2 + half) * (kBlk * D) + 16 * u) = out;
+      out = u32x4{w[0], w[1], w[2], w[3]};
     }
+    *reinterpret_cast<u32x4*>(a.pages + ((int64_t)page * 2 + half) * (kBlk * D) + 16 * u) = out;
     if (u == 0) a.scales[(int64_t)page * 2 + half] = finite ? (float)((double)amax / 127.0) : quiet_nan();
   }
   // The new rows of the block that stays open.  The workgroup of the first
@@ -144,8 +158,8 @@ __global__ __launch_bounds__(kKvThreads) void k_kv_append(CacheArgs a, int count
 }
 
 template <typename T, int D>
-__global__ __launch_bounds__(kKvThreads) void k_kv_read(CacheArgs a, int count) {
-  constexpr int V = Vec<T>::N, CH = D / V;
+__global__ __launch_bounds__(kv_threads(D)) void k_kv_read(CacheArgs a, int count) {
+  constexpr int kKvThreads = kv_threads(D), V = Vec<T>::N, CH = D / V;
   constexpr int kRow = D + 16;
   __shared__ alignas(16) uint8_t codes[kBlk * kRow];
   const int j = blockIdx.x % count;
@@ -173,19 +187,17 @@ __global__ __launch_bounds__(kKvThreads) void k_kv_read(CacheArgs a, int count) 
   if (good) {
     scale = a.scales[(int64_t)page * 2 + half];
     scale = scale >= 0.f ? scale : quiet_nan();
-    if (u < 2 * D) {
-      const u32x4 v = ld16(a.pages + ((int64_t)page * 2 + half) * (kBlk * D) + 16 * u);
-      int t, e;
-      if (half == 0) {
-        Unit<D>::key(u, t, e);
-        *reinterpret_cast<u32x4*>(codes + t * kRow + e) = v;
-      } else {
-        const unsigned w[4] = {v.x, v.y, v.z, v.w};
+    const u32x4 v = ld16(a.pages + ((int64_t)page * 2 + half) * (kBlk * D) + 16 * u);
+    int t, e;
+    if (half == 0) {
+      Unit<D>::key(u, t, e);
+      *reinterpret_cast<u32x4*>(codes + t * kRow + e) = v;
+    } else {
+      const unsigned w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          Unit<D>::value(u, k, t, e);
-          codes[t * kRow + e] = (uint8_t)(w[k / 4] >> 8 * (k % 4));
-        }
+      for (int k = 0; k < 16; ++k) {
+        Unit<D>::value(u, k, t, e);
+        codes[t * kRow + e] = (uint8_t)(w[k / 4] >> 8 * (k % 4));
       }
     }
   }
@@ -218,7 +230,7 @@ hipError_t launch_kv_append(const CacheArgs& a, hipStream_t s) {
   const int count = touched_blocks(a.max_new);
   const dim3 grid((unsigned)a.n_seqs * a.hk * 2 * count);
   return by_type(a, [&](auto t, auto d) {
-    k_kv_append<decltype(t), decltype(d)::value><<<grid, kKvThreads, 0, s>>>(a, count);
+    k_kv_append<decltype(t), decltype(d)::value><<<grid, kv_threads(decltype(d)::value), 0, s>>>(a, count);
   });
 }
 
@@ -226,7 +238,7 @@ hipError_t launch_kv_read(const CacheArgs& a, hipStream_t s) {
   const int count = touched_blocks(a.max_new);
   const dim3 grid((unsigned)a.n_seqs * a.hk * 2 * count);
   return by_type(a, [&](auto t, auto d) {
-    k_kv_read<decltype(t), decltype(d)::value><<<grid, kKvThreads, 0, s>>>(a, count);
+    k_kv_read<decltype(t), decltype(d)::value><<<grid, kv_threads(decltype(d)::value), 0, s>>>(a, count);
   });
 }
 
