@@ -16,8 +16,8 @@
 // 16-byte load, 1 KB in a row for a wave.
 //
 // Two ways to cut the work, by size (attend_plan).  Few rows (k_attend): the
-// pages' bytes bound the time; the four waves of a workgroup share the rows
-// and take every fourth block.  Many rows (k_attend_many): the weights' exponentials and the
+// pages' bytes bound the time; the eight waves of a workgroup share the rows
+// and take every eighth block.  Many rows (k_attend_many): the weights' exponentials and the
 // products do; each wave has rows of its own and all walk the blocks in
 // step, whose codes are turned to fp16 once for the workgroup, in LDS.  Both
 // split the blocks over workgroups as well where the rows do not fill the
@@ -31,8 +31,8 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 typedef float f32x8 __attribute__((ext_vector_type(8)));
 
-constexpr int kAtThreads = 256;
-constexpr int kAtWaves = kAtThreads / kWave;
+constexpr int kAtThreads = 256;              // k_attend_join
+constexpr int kFewThreads = 512, kFewWaves = kFewThreads / kWave;
 constexpr int kManyThreads = 512;
 constexpr int kManyWaves = kManyThreads / kWave;
 constexpr int kMaxSplits = 64;
@@ -373,12 +373,12 @@ __device__ __forceinline__ void store4(T* p, f32x4 v) {
 }
 
 template <typename T, int D, int NB, bool SCORE>
-__global__ __launch_bounds__(kAtThreads, 2) void k_attend(AttendArgs a) {
+__global__ __launch_bounds__(kFewThreads, 2) void k_attend(AttendArgs a) {
   constexpr int KK = D / 64, DT = D / 16, DB = D / 32;
   const Walk w(a);
   const int lane = lane_id(), wave = wave_id(), g = lane / 16, c = lane % 16;
   if (!w.q.ok) {
-    if (w.split == 0) nan_rows<T>(a, w.q, w.h, D, (int64_t)w.tile * kAtThreads + threadIdx.x, (int64_t)a.tiles * kAtThreads);
+    if (w.split == 0) nan_rows<T>(a, w.q, w.h, D, (int64_t)w.tile * kFewThreads + threadIdx.x, (int64_t)a.tiles * kFewThreads);
     if (threadIdx.x == 0) raise_flag(a.flags, PI_FLAG_KV_RANGE);
     return;
   }
@@ -390,7 +390,7 @@ __global__ __launch_bounds__(kAtThreads, 2) void k_attend(AttendArgs a) {
   const int per = (nbk + a.splits - 1) / a.splits;
   const int b0 = w.split * per, b1 = b0 + per < nbk ? b0 + per : nbk;
   const int start = b0 + wave;
-  const int mine = start < b1 ? (b1 - start + kAtWaves - 1) / kAtWaves : 0;
+  const int mine = start < b1 ? (b1 - start + kFewWaves - 1) / kFewWaves : 0;
 
   // The weights as two parts: the products have time while the pages come.
   Rows<T, D, NB, SCORE, true> rows;
@@ -400,7 +400,7 @@ __global__ __launch_bounds__(kAtThreads, 2) void k_attend(AttendArgs a) {
   Blocks x;
   for (int base = 0; base < mine; base += kWave) {
     const int cnt = mine - base < kWave ? mine - base : kWave;
-    x.find(a, w.pair, start + base * kAtWaves, kAtWaves, cnt, bad);
+    x.find(a, w.pair, start + base * kFewWaves, kFewWaves, cnt, bad);
     auto page_at = [&](int i) {
       return a.pages + (int64_t)__builtin_amdgcn_readlane(x.page, i) * (2 * kBlk * D) + lane * 16;
     };
@@ -427,7 +427,7 @@ __global__ __launch_bounds__(kAtThreads, 2) void k_attend(AttendArgs a) {
     for (int i = 0; i < cnt; ++i) {
       const int n = i + 1 < kWave ? i + 1 : i;
       rows.block(
-          a, w, x, i, start + (base + i) * kAtWaves, kmin,
+          a, w, x, i, start + (base + i) * kFewWaves, kmin,
           [&](int mb, int kk, int f) {
             const u32x4 v = rk[mb * KK + kk];
             return f ? codes_f16(v.z, v.w) : codes_f16(v.x, v.y);
@@ -443,11 +443,11 @@ __global__ __launch_bounds__(kAtThreads, 2) void k_attend(AttendArgs a) {
   raise_flag_if_any(a.flags, bad, PI_FLAG_KV_RANGE);
   rows.finish();
 
-  // The four waves' sums, added in wave order.
-  __shared__ float so[kAtWaves][16][D + 4];
-  __shared__ float sm[kAtWaves][16], sl[kAtWaves][16];
-  constexpr int E = D / 16;                         // elements of a thread
-  const int row = threadIdx.x / 16, e0 = threadIdx.x % 16 * E;
+  // The waves' sums, added in wave order.
+  __shared__ float so[kFewWaves][16][D + 4];
+  __shared__ float sm[kFewWaves][16], sl[kFewWaves][16];
+  constexpr int E = D * 16 / kFewThreads > 4 ? D * 16 / kFewThreads : 4;     // elements of a thread
+  const int row = threadIdx.x / (D / E), e0 = threadIdx.x % (D / E) * E;
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb) {
     if (nb) __syncthreads();
@@ -456,15 +456,15 @@ __global__ __launch_bounds__(kAtThreads, 2) void k_attend(AttendArgs a) {
     if (g == 0) sm[wave][c] = rows.m[nb], sl[wave][c] = rows.l[nb];
     __syncthreads();
     const int r = r0 + nb * 16 + row;
-    if (r >= w.rows) continue;
+    if (row >= 16 || r >= w.rows) continue;
     float top = sm[0][row];
 #pragma unroll
-    for (int y = 1; y < kAtWaves; ++y) top = fmaxf(top, sm[y][row]);
+    for (int y = 1; y < kFewWaves; ++y) top = fmaxf(top, sm[y][row]);
     float sum = 0.f, v[E];
 #pragma unroll
     for (int k = 0; k < E; ++k) v[k] = 0.f;
 #pragma unroll
-    for (int y = 0; y < kAtWaves; ++y) {
+    for (int y = 0; y < kFewWaves; ++y) {
       const float f = exp2_hw(sm[y][row] - top);
       sum = __builtin_fmaf(f, sl[y][row], sum);
 #pragma unroll
@@ -741,8 +741,8 @@ hipError_t attend_run(const AttendArgs& a, hipStream_t s) {
     if (a.score) k_attend_many<T, D, NB, true, 1><<<grid, kManyThreads, 0, s>>>(a);
     else k_attend_many<T, D, NB, false, G><<<grid, G * kManyThreads, 0, s>>>(a);
   } else {
-    if (a.score) k_attend<T, D, NB, true><<<grid, kAtThreads, 0, s>>>(a);
-    else k_attend<T, D, NB, false><<<grid, kAtThreads, 0, s>>>(a);
+    if (a.score) k_attend<T, D, NB, true><<<grid, kFewThreads, 0, s>>>(a);
+    else k_attend<T, D, NB, false><<<grid, kFewThreads, 0, s>>>(a);
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || (a.splits == 1 && !a.score)) return e;
@@ -782,10 +782,10 @@ AttendPlan attend_plan(int n_seqs, int hk, int group, int d, int dtype, int max_
   const int wg_rows = narrow * p.nb;
   p.tiles = (p.r_max + wg_rows - 1) / wg_rows;
   const int64_t wgs = pairs * p.tiles;
-  // Splits as long as all workgroups run at once (one a CU of k_attend_many's,
-  // two of k_attend's): 8 x 32 pairs of 8192 tokens, D = 128, 98 us with four
-  // splits and 93 with two; 56 x 4 pairs of 4001 tokens in fp32 48 us with five, 42 with two.
-  int64_t splits = (p.many ? 256 : 512) / wgs;
+  // Splits as long as all workgroups run at once, one a CU: 8 x 32 pairs of
+  // 8192 tokens, D = 128, 91.9 us without and 96.3 with two; 56 x 4 pairs of
+  // 4001 tokens in fp32 38.9 us without and 45.2 with two.
+  int64_t splits = 256 / wgs;
   const int64_t most = (p.max_nb + 7) / 8;
   splits = splits < most ? splits : most;
   splits = splits < kMaxSplits ? splits : kMaxSplits;
