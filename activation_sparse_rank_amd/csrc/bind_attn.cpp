@@ -9,6 +9,7 @@
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
+#include <c10/core/DeviceGuard.h>
 #include <c10/hip/HIPStream.h>
 #include <dlfcn.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -101,9 +102,11 @@ void* stream_of(PyObject* o, int dev) {
   return p;
 }
 
-// Other Python threads run while a call is queued (a full queue makes it wait).
+// The call itself, with device dev current.  Other Python threads run while it
+// is queued (a full queue makes it wait).
 template <typename F>
-int64_t unlocked(F f) {
+int64_t queue(int dev, F f) {
+  const c10::DeviceGuard guard(c10::Device(c10::kCUDA, (c10::DeviceIndex)dev));
   pi_status st;
   Py_BEGIN_ALLOW_THREADS;
   st = f();
@@ -152,7 +155,7 @@ int64_t qk_rope(PyObject* const* a, Py_ssize_t n) {
   const int32_t* pos = int32s(a[4], "pos", q.n_tok, dev);
   if (q.n_tok == 0) return PI_OK;
   void* s = stream_of(a[7], dev);
-  return unlocked([&] {
+  return queue(dev, [&] {
     return lib.qk_rope(r, q.p, q.ts, q.hs, q.heads, k.p, k.ts, k.hs, k.heads, pos, q.n_tok,
                        dt == at::kHalf ? PI_F16 : PI_F32, qo.p, qo.ts, qo.hs, ko.p, ko.ts, ko.hs, s);
   });
@@ -171,7 +174,7 @@ int64_t kv_rows(PyObject* const* a, Py_ssize_t n) {
   const Bounds b = bounds(c, a[4], a[5], a[6], k.n_tok, dev);
   if (k.n_tok == 0) return PI_OK;
   void* s = stream_of(a[7], dev);
-  return unlocked([&] {
+  return queue(dev, [&] {
     return READ ? lib.kv_read(c, b.lens, b.q_start, b.max_q, k.p, k.ts, k.hs, v.p, v.ts, v.hs, k.n_tok, s)
                 : lib.kv_append(c, k.p, k.ts, k.hs, v.p, v.ts, v.hs, k.n_tok, b.lens, b.q_start, b.max_q, s);
   });
@@ -194,7 +197,7 @@ int64_t attend(PyObject* const* a, Py_ssize_t n) {
   if (add_score && !c->score) fail(PyExc_ValueError, "%s needs a cache with a score", "add_score");
   if (q.n_tok == 0) return PI_OK;
   void* s = stream_of(a[11], dev);
-  return unlocked([&] {
+  return queue(dev, [&] {
     return lib.attend(c, q.p, q.ts, q.hs, q.heads, q.n_tok, b.lens, b.q_start, b.max_q, max_len, scale, add_score,
                       out.p, out.ts, out.hs, ws.data_ptr(), (size_t)ws.numel(), s);
   });
@@ -229,7 +232,7 @@ int64_t kv_evict(PyObject* const* a, Py_ssize_t n) {
   int32_t* lens_out = int32s(a[5], "lens_out", table.size(0), dev);
   const int keep = (int)integer(a[3], "keep"), recent = (int)integer(a[4], "recent");
   void* st = stream_of(a[8], dev);
-  return unlocked([&] {
+  return queue(dev, [&] {
     return lib.kv_evict(t, s, lens, (int)table.size(0), (int)table.size(1), (int)table.size(2), keep, recent, to, so,
                         lens_out, st);
   });

@@ -36,7 +36,7 @@ constexpr int kFewThreads = 512, kFewWaves = kFewThreads / kWave;
 constexpr int kManyThreads = 512;
 constexpr int kManyWaves = kManyThreads / kWave;
 constexpr int kMaxSplits = 64;
-constexpr float kNoMax = -1e30f;     // reference before the first visible token
+constexpr float kNoMax = -3e38f;     // reference before the first visible token
 // Weights are held times 2^6, and a lane's eight of a block may sum to 2^15
 // (fp16 holds 65504) before the reference moves: no maximum is taken but
 // then.  What a weight loses below fp16's smallest step is at most 2^-31 of the

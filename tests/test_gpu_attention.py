@@ -490,6 +490,86 @@ def test_attend_streams_and_graph():
         assert torch.equal(eager, refs[(rep + 1) % 3])
 
 
+def test_attend_huge_logits():
+    """fp32 logits far below -1e30 are logits still.  (One block: between blocks
+    the weights hold to half a step of the logits, which is 1e26 here.)"""
+    d = 64
+    c = Cache(1, 1, d, 3, f32)
+    k, v = _rows(30, 1, d, f32, 4)
+    c.append(torch.ones_like(k), v, (30,))                       # every key the same: equal weights
+    q = torch.full((1, 1, d), -1e33, device=DEV)
+    ln = torch.tensor([30], dtype=torch.int32, device=DEV)
+    out, _ = _attend(c, q, ln, torch.tensor([0, 1], dtype=torch.int32, device=DEV), 1)
+    _, vals = c.values(0, 0)
+    assert np.abs(host(out)[0, 0] - vals.mean(0)).max() <= 2.0 ** -18 * np.abs(vals).max()
+
+
+@pytest.mark.parametrize("how", ["object", "handle"])
+def test_a_step_on_a_stream_of_its_own_and_in_a_graph(how):
+    """Rotation, append, attention, eviction, in a row, on the stream that is
+    given; then replayed from a graph with eager steps between, each replay
+    against the eager step from the same state."""
+    seqs, hk, group, d, keep, recent = 2, 2, 4, 64, 3, 1
+    c = Cache(seqs, hk, d, 8, f16, score=True)
+    k, v = _rows(150, hk, d, f16, 1)
+    lens, _ = c.append(k, v, (90, 60))
+    c.scales.nan_to_num_(nan=1.0)                                # spare pages: no NaN to compare
+    c.open.nan_to_num_(nan=0.0)
+    r = pi.Rope(torch.from_numpy(_freqs(d)).to(DEV), d)
+    qkv = torch.empty((seqs, (group * hk + 2 * hk) * d), dtype=f16, device=DEV)
+    q, kk, vv = (t.unflatten(1, (-1, d)) for t in qkv.split((group * hk * d, hk * d, hk * d), 1))
+    pos = torch.tensor([90, 60], dtype=torch.int32, device=DEV)
+    qs = torch.arange(seqs + 1, dtype=torch.int32, device=DEV)
+    out = torch.zeros((seqs, group * hk, d), dtype=f16, device=DEV)
+    held = torch.zeros_like(lens)
+    now = lens + 1
+    ws = pi.alloc_attend_workspace(c.c, group * hk, 1, add_score=True)
+    xs = [torch.randn(qkv.shape, device=DEV).to(f16) for _ in range(3)]
+    state = (c.pages, c.scales, c.open, c.table, c.score)
+    first = [t.clone() for t in state]
+    torch.cuda.synchronize()
+
+    def step(s):
+        pi.qk_rope(r, q, kk, pos, stream=s)
+        pi.kv_append(c.c, kk, vv, now, q_start=qs, max_new=1, stream=s)
+        pi.attend(c.c, q, now, out, q_start=qs, max_q=1, add_score=True, ws=ws, stream=s)
+        pi.kv_evict(c.table, c.score, now, keep, recent, held, stream=s)
+
+    def reset(i):
+        for t, f in zip(state, first):
+            t.copy_(f)
+        qkv.copy_(xs[i])
+        out.zero_(), held.zero_()
+        torch.cuda.synchronize()
+
+    def seen():
+        torch.cuda.synchronize()
+        return [t.clone() for t in (*state, qkv, out, held)]
+
+    stream = torch.cuda.Stream()
+    given = stream if how == "object" else stream.cuda_stream
+    want = []
+    for i in range(3):
+        reset(i)
+        step(None)
+        want.append(seen())
+        reset(i)
+        step(given)
+        assert all(torch.equal(a, b) for a, b in zip(seen(), want[i])), i
+    reset(0)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        step(None)
+    for rep in range(6):
+        reset(rep % 3)
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip(seen(), want[rep % 3])), rep
+        reset((rep + 1) % 3)
+        step(None)
+        assert all(torch.equal(a, b) for a, b in zip(seen(), want[(rep + 1) % 3])), rep
+    assert pi.read_flags(ws) == 0
+
+
 # ---- eviction -------------------------------------------------------------
 
 @pytest.mark.parametrize("seqs,hk,n,keep,recent", [(1, 1, 1, 1, 1), (3, 2, 130, 96, 8), (2, 3, 1024, 40, 40), (2, 1, 4099, 2048, 32),
