@@ -292,10 +292,11 @@ struct Rows {
           for (int j = 0; j < 4; ++j) st[nb][mb][j] = mb * 16 + j < left ? st[nb][mb][j] * sc : -__builtin_inff();
       }
     }
+    const float scv = edge ? 1.f : ksc;
     f16x8 pf[NB], pl[NB];
     float sum[NB];
     auto weights = [&](int nb) {
-      const float sc = edge ? 1.f : scale_of(nb), off = lrb - m[nb];
+      const float sc = kTwo ? (edge ? 1.f : ksc * rs[nb]) : scv, off = lrb - m[nb];
       float p[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) p[j] = exp2_hw(__builtin_fmaf(st[nb][j / 4][j % 4], sc, off));
@@ -514,6 +515,7 @@ __global__ __launch_bounds__(G * kManyThreads, 2 * G) void k_attend_many(AttendA
 
   __shared__ u32x4 ops[2][kStep][kUnits][2][kWave];
   Rows<T, D, NB, SCORE, sizeof(T) == 4> rows;
+  f16x8 vals[DT];                                   // a block's values, on their way while its weights are taken
   rows.load(a, w, r0);
   bool bad = false;
   Blocks x;
@@ -544,8 +546,12 @@ __global__ __launch_bounds__(G * kManyThreads, 2 * G) void k_attend_many(AttendA
         if (i + j < cnt && b * kBlk < kmax)
           rows.block(
               a, w, x, i + j, b, kmin,
-              [&](int mb, int kk, int f) { return __builtin_bit_cast(f16x8, ops[buf][j][mb * KK + kk][f][lane]); }, [] {},
-              [&](int t) { return __builtin_bit_cast(f16x8, ops[buf][j][2 * KK + t / 2][t % 2][lane]); });
+              [&](int mb, int kk, int f) { return __builtin_bit_cast(f16x8, ops[buf][j][mb * KK + kk][f][lane]); },
+              [&] {
+#pragma unroll
+                for (int t = 0; t < DT; ++t) vals[t] = __builtin_bit_cast(f16x8, ops[buf][j][2 * KK + t / 2][t % 2][lane]);
+              },
+              [&](int t) { return vals[t]; });
       }
       buf ^= 1;
       if (more) turn(buf, next);
