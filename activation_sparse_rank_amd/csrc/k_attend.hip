@@ -70,14 +70,21 @@ __device__ __forceinline__ float lane_f(float v, int lane) {
   return as_f((unsigned)__builtin_amdgcn_readlane((int)__builtin_bit_cast(unsigned, v), lane));
 }
 
-// Sum and maximum over the four lanes that hold a row (lane % 16).
+// Sum and maximum over the four lanes that hold a row (lane % 16): a value's
+// rows of 16 (32) lanes are swapped with a copy's, which leaves both partners in every lane.
+template <typename F>
+__device__ __forceinline__ float over_row(float v, F f) {
+  const unsigned a = __builtin_bit_cast(unsigned, v);
+  const auto x = __builtin_amdgcn_permlane16_swap(a, a, false, false);
+  const unsigned b = __builtin_bit_cast(unsigned, f(as_f(x[0]), as_f(x[1])));
+  const auto y = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+  return f(as_f(y[0]), as_f(y[1]));
+}
 __device__ __forceinline__ float row_sum(float v) {
-  v += __shfl_xor(v, 16, kWave);
-  return v + __shfl_xor(v, 32, kWave);
+  return over_row(v, [](float a, float b) { return a + b; });
 }
 __device__ __forceinline__ float row_max(float v) {
-  v = fmaxf(v, __shfl_xor(v, 16, kWave));
-  return fmaxf(v, __shfl_xor(v, 32, kWave));
+  return over_row(v, [](float a, float b) { return fmaxf(a, b); });
 }
 
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
@@ -620,10 +627,14 @@ __device__ __forceinline__ float2 row_ml(const AttendArgs& a, int pairs, int pai
 }
 
 // Joins the splits' sums into rows (workgroups below row_groups: kFewSplits
-// splits or less, a thread adds them and a workgroup takes as many rows as it has
-// threads for; more, a workgroup takes one row and shares the splits) and adds the blocks' weights to the score (the others, kScoreBlocks blocks
-// of a (sequence, kv head) each).
-constexpr int kScoreBlocks = 64;
+// splits or less, a thread adds them and a workgroup takes as many rows as it
+// has threads for; more, a workgroup takes one row and shares the splits), and
+// adds the blocks' weights to the score (the others, kAtThreads / score_lanes()
+// blocks of a (sequence, kv head) each).
+//
+// Lanes that share a block's rows: few where the rows are few, else a wave,
+// which reads 64 rows of a block at once (2000 rows x 8 pairs, 63 blocks: 1006 us with four).
+__host__ __device__ constexpr int score_lanes(int r_max) { return r_max > 32 ? kWave : 4; }
 constexpr int kFewSplits = 8;
 template <typename T, int D>
 __global__ __launch_bounds__(kAtThreads) void k_attend_join(AttendArgs a, int row_groups) {
@@ -697,16 +708,26 @@ __global__ __launch_bounds__(kAtThreads) void k_attend_join(AttendArgs a, int ro
     store4(p, o);
     return;
   }
-  const int per = (a.max_nb + kScoreBlocks - 1) / kScoreBlocks;
-  const int pair = (blockIdx.x - row_groups) / per, first = (blockIdx.x - row_groups) % per * kScoreBlocks;
+  const int lanes = score_lanes(a.r_max), each = kAtThreads / lanes;
+  const int per = (a.max_nb + each - 1) / each;
+  const int pair = (blockIdx.x - row_groups) / per, first = (blockIdx.x - row_groups) % per * each;
   const Seq q = read_seq(a.lens, a.q_start, pair / a.hk, a.max_q, a.n_tok, a.max_len);
   if (!q.ok || first * kBlk >= q.len) return;
-  constexpr int kChunk = 256, Q = kAtThreads / kScoreBlocks;
+  constexpr int kChunk = kAtThreads;
   __shared__ float lse[kChunk];
   const int rows = q.n * a.group, seen0 = q.len - q.n + 1;
-  const int b = first + threadIdx.x / Q, sub = threadIdx.x % Q;
+  // The first row that sees a token of block b (the rows after it do too).
+  auto first_row = [&](int b) {
+    const int64_t t = (int64_t)b * kBlk + 1 - seen0;
+    const int64_t r = t > 0 ? t * a.group : 0;
+    return r < rows ? (int)r : rows;
+  };
+  const int b = first + threadIdx.x / lanes, sub = threadIdx.x % lanes;
+  const int from_row = first_row(b);
+  const bool held = b * kBlk < q.len;
+  const float* from = a.lse + ((int64_t)pair * a.max_nb + (held ? b : 0)) * a.r_max;
   float w = 0.f;
-  for (int c0 = 0; c0 < rows; c0 += kChunk) {
+  for (int c0 = first_row(first) / kChunk * kChunk; c0 < rows; c0 += kChunk) {
     __syncthreads();
     const int r = c0 + threadIdx.x;
     if (r < rows) {
@@ -714,15 +735,14 @@ __global__ __launch_bounds__(kAtThreads) void k_attend_join(AttendArgs a, int ro
       lse[threadIdx.x] = v.x + log2_hw(v.y);
     }
     __syncthreads();
-    if (b * kBlk < q.len) {
-      const float* from = a.lse + ((int64_t)pair * a.max_nb + b) * a.r_max;
-      for (int k = sub; k < kChunk && c0 + k < rows; k += Q)
-        if (b * kBlk < seen0 + (c0 + k) / a.group) w += exp2_hw(from[c0 + k] - lse[k]);
+    if (held) {
+      const int end = rows - c0 < kChunk ? rows - c0 : kChunk;
+      for (int k = sub; k < end; k += lanes)
+        if (c0 + k >= from_row) w += exp2_hw(from[c0 + k] - lse[k]);
     }
   }
-#pragma unroll
-  for (int x = 1; x < Q; x <<= 1) w += __shfl_xor(w, x, kWave);
-  if (sub == 0 && b * kBlk < q.len) a.score[(int64_t)pair * a.max_blocks + b] += w;
+  for (int x = 1; x < lanes; x <<= 1) w += __shfl_xor(w, x, kWave);
+  if (sub == 0 && held) a.score[(int64_t)pair * a.max_blocks + b] += w;
 }
 
 // 16-row tiles of a wave: what its registers hold, beside the pages' codes in k_attend.
@@ -754,7 +774,8 @@ hipError_t attend_run(const AttendArgs& a, hipStream_t s) {
   if (e != hipSuccess || (a.splits == 1 && !a.score)) return e;
   const int each = a.splits <= kFewSplits ? kAtThreads / (D / 4) : 1;      // rows of a workgroup
   const int row_groups = a.splits > 1 ? (int)(((int64_t)pairs * a.r_max + each - 1) / each) : 0;
-  const int score_groups = a.score ? pairs * ((a.max_nb + kScoreBlocks - 1) / kScoreBlocks) : 0;
+  const int blocks = kAtThreads / score_lanes(a.r_max);                    // blocks of a workgroup
+  const int score_groups = a.score ? pairs * ((a.max_nb + blocks - 1) / blocks) : 0;
   k_attend_join<T, D><<<dim3((unsigned)row_groups + score_groups), kAtThreads, 0, s>>>(a, row_groups);
   return hipGetLastError();
 }
