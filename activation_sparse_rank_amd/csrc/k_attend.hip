@@ -22,6 +22,14 @@
 // step, whose codes are turned to fp16 once for the workgroup, in LDS.  Both
 // split the blocks over workgroups as well where the rows do not fill the
 // CUs; partial sums are joined in a fixed order (in LDS, then in k_attend_join).
+//
+// Measured (streaming read 6.45 TB/s, fp16 product 1150 TFLOP/s on the same
+// card): one token of 64 heads over 131072 tokens of 8 kv heads, D = 128, 48.0 us with
+// the join (269 MB, 5.6 TB/s); 32 sequences of 16384 tokens and less with
+// scores 152 us (863 MB, 5.7 TB/s); fp32, 56 kv heads of their own, 33.9 us (180 MB, 5.3
+// TB/s); 512 tokens of 128 heads over 8200 tokens, D = 64, 158 us (133 GFLOP,
+// 844 TFLOP/s): there the instructions around the products bind, 230 k cycles
+// a SIMD beside the products' 127 k, of 350 k.
 #include "attn_device.h"
 
 namespace pi {

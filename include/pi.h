@@ -1,6 +1,7 @@
 /*
  * pi.h -- C ABI of libpi: a predictor-gated, neuron-aware sparse FFN for one
- * AMD MI355X (gfx950).
+ * AMD MI355X (gfx950), and the attention side of a decode layer beside it (rotary
+ * positions, an 8-bit key/value cache, attention over it, eviction).
  *
  * The method (PowerInfer, as three web pages describe it):
  *  - [QB] QbitAI article on r-manual.ru, "2080 Ti может запускать большие
@@ -437,7 +438,8 @@ pi_status pi_kv_read(const pi_kv_cache* cache, const int32_t* lens, const int32_
 
 /* Bytes of workspace that pi_attend needs for these bounds; 0 for invalid
  * arguments.  add_score asks for 4 bytes per row, kv head and block more:
- * n_seqs * max_q * n_heads * ceil(max_len / PI_KV_BLOCK) * 4.  */
+ * n_seqs * max_q * n_heads * ceil(max_len / PI_KV_BLOCK) * 4.  (A long prompt
+ * with scores is better appended and attended in chunks.)  */
 size_t pi_attend_workspace_bytes(const pi_kv_cache* cache, int32_t n_heads, int32_t max_q, int32_t max_len,
                                  int32_t add_score);
 
@@ -446,8 +448,9 @@ size_t pi_attend_workspace_bytes(const pi_kv_cache* cache, int32_t n_heads, int3
  * Row i of a sequence's new rows sees tokens 0 .. lens - new + i (itself the
  * last); a row that sees none gives zeros.  Logits, the softmax's statistics
  * and all sums are fp32.  fp16: queries and codes enter the products
- * unrounded, weights are rounded to fp16 once.  fp32: queries and weights
- * enter as two fp16 parts (22 significant bits).
+ * unrounded, weights as fp16 (few rows: as two fp16 parts).  fp32: queries and
+ * weights enter as two fp16 parts (22 significant bits).  A weight holds to
+ * half a step of its logit in fp32, as any fp32 softmax's.
  *   q, out:    [n_tok][n_heads][head_dim]; out must not overlap q
  *   max_q:     host bound on the new rows of a sequence (1: decode)
  *   max_len:   host bound on lens, in [1, max_blocks * PI_KV_BLOCK]

@@ -19,6 +19,9 @@ Sources (three web pages about PowerInfer, from SJTU-IPADS):
        70B, а новая платформа может увеличить скорость вывода LLM в 11 раз".
   [AB] aibars.net library profile "SJTU-IPADS/PowerInfer" (Portuguese).
 
+``oracle.attention`` holds the attention side (rotation, the 8-bit cache,
+attention, eviction); tests/test_attention_oracle.py pins it.
+
 Every function is pinned by a CPU test against something other than itself
 (pure-Python brute force, hand-worked fixtures under tests/golden/, closed
 forms and invariants).  No function here is "parity unpinned".
