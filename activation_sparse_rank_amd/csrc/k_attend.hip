@@ -462,6 +462,7 @@ __global__ __launch_bounds__(kFewThreads, 2) void k_attend(AttendArgs a) {
   // The waves' sums, added in wave order.
   __shared__ float so[kFewWaves][16][D + 4];
   __shared__ float sm[kFewWaves][16], sl[kFewWaves][16];
+  __shared__ float rl[SCORE ? NB * 16 : 1];         // log2 of a row's weights, where this workgroup has all of them
   constexpr int E = D * 16 / kFewThreads > 4 ? D * 16 / kFewThreads : 4;     // elements of a thread
   const int row = threadIdx.x / (D / E), e0 = threadIdx.x % (D / E) * E;
 #pragma unroll
@@ -496,7 +497,28 @@ __global__ __launch_bounds__(kFewThreads, 2) void k_attend(AttendArgs a) {
       if (whole) store4(p + k, y * inv);
       else *reinterpret_cast<f32x4*>(a.part + at * D + e0 + k) = y;
     }
-    if ((!whole || SCORE) && e0 == 0) a.ml[at] = float2{top, sum};
+    if (!whole && e0 == 0) a.ml[at] = float2{top, sum};
+    if (SCORE && e0 == 0) {
+      if (a.tiles > 1) a.ml[at] = float2{top, sum};
+      rl[nb * 16 + row] = top + log2_hw(sum);
+    }
+  }
+  if constexpr (SCORE) {
+    // The blocks' weights are in the workspace, from this workgroup's waves.
+    if (a.splits > 1 || a.tiles > 1) return;
+    __threadfence_block();
+    __syncthreads();
+    constexpr int Q = 4;                            // lanes that share a block's rows
+    const int sub = threadIdx.x % Q;
+    for (int b = threadIdx.x / Q; b < nbk; b += kFewThreads / Q) {
+      const float* from = a.lse + ((int64_t)w.pair * a.max_nb + b) * a.r_max;
+      float sum = 0.f;
+      for (int r = sub; r < w.rows; r += Q)
+        if (b * kBlk < w.sees(a, r)) sum += exp2_hw(from[r] - rl[r]);
+      sum += __shfl_xor(sum, 1, kWave);
+      sum += __shfl_xor(sum, 2, kWave);
+      if (sub == 0) a.score[(int64_t)w.pair * a.max_blocks + b] += sum;
+    }
   }
 }
 
@@ -640,9 +662,12 @@ __device__ __forceinline__ float2 row_ml(const AttendArgs& a, int pairs, int pai
 // adds the blocks' weights to the score (the others, kAtThreads / score_lanes()
 // blocks of a (sequence, kv head) each).
 //
-// Lanes that share a block's rows: few where the rows are few, else a wave,
-// which reads 64 rows of a block at once (2000 rows x 8 pairs, 63 blocks: 1006 us with four).
-__host__ __device__ constexpr int score_lanes(int r_max) { return r_max > 32 ? kWave : 4; }
+// Lanes that share a block's rows: few where the rows are few, a wave where the
+// rows' sums over the splits are worth sharing among blocks, else the workgroup
+// (2000 rows x 8 pairs, 63 blocks: 1006 us with four lanes, 100 with a wave, 14 so).
+__host__ __device__ constexpr int score_lanes(int r_max, int splits) {
+  return r_max <= 32 ? 4 : (splits > 1 ? kWave : kAtThreads);
+}
 constexpr int kFewSplits = 8;
 template <typename T, int D>
 __global__ __launch_bounds__(kAtThreads) void k_attend_join(AttendArgs a, int row_groups) {
@@ -716,40 +741,52 @@ __global__ __launch_bounds__(kAtThreads) void k_attend_join(AttendArgs a, int ro
     store4(p, o);
     return;
   }
-  const int lanes = score_lanes(a.r_max), each = kAtThreads / lanes;
+  const int lanes = score_lanes(a.r_max, a.splits), each = kAtThreads / lanes;
   const int per = (a.max_nb + each - 1) / each;
   const int pair = (blockIdx.x - row_groups) / per, first = (blockIdx.x - row_groups) % per * each;
   const Seq q = read_seq(a.lens, a.q_start, pair / a.hk, a.max_q, a.n_tok, a.max_len);
   if (!q.ok || first * kBlk >= q.len) return;
-  constexpr int kChunk = kAtThreads;
-  __shared__ float lse[kChunk];
   const int rows = q.n * a.group, seen0 = q.len - q.n + 1;
-  // The first row that sees a token of block b (the rows after it do too).
-  auto first_row = [&](int b) {
-    const int64_t t = (int64_t)b * kBlk + 1 - seen0;
-    const int64_t r = t > 0 ? t * a.group : 0;
-    return r < rows ? (int)r : rows;
-  };
   const int b = first + threadIdx.x / lanes, sub = threadIdx.x % lanes;
-  const int from_row = first_row(b);
   const bool held = b * kBlk < q.len;
+  // The first row that sees a token of block b (the rows after it do too).
+  const int64_t t = (int64_t)b * kBlk + 1 - seen0, r0 = t > 0 ? t * a.group : 0;
   const float* from = a.lse + ((int64_t)pair * a.max_nb + (held ? b : 0)) * a.r_max;
   float w = 0.f;
-  for (int c0 = first_row(first) / kChunk * kChunk; c0 < rows; c0 += kChunk) {
-    __syncthreads();
-    const int r = c0 + threadIdx.x;
-    if (r < rows) {
-      const float2 v = row_ml(a, pairs, pair, r);
-      lse[threadIdx.x] = v.x + log2_hw(v.y);
+  if (lanes == kAtThreads) {
+    if (held && r0 < rows) {
+#pragma unroll 4
+      for (int r = (int)r0 + sub; r < rows; r += kAtThreads) {
+        const float2 v = row_ml(a, pairs, pair, r);
+        w += exp2_hw(from[r] - v.x - log2_hw(v.y));
+      }
     }
-    __syncthreads();
-    if (held) {
-      const int end = rows - c0 < kChunk ? rows - c0 : kChunk;
-      for (int k = sub; k < end; k += lanes)
-        if (c0 + k >= from_row) w += exp2_hw(from[c0 + k] - lse[k]);
+  } else {
+    __shared__ float lse[kAtThreads];               // of a chunk of the rows, for all the workgroup's blocks
+    const int64_t t0 = (int64_t)first * kBlk + 1 - seen0, low = t0 > 0 ? t0 * a.group : 0;
+    for (int64_t c0 = low / kAtThreads * kAtThreads; c0 < rows; c0 += kAtThreads) {
+      __syncthreads();
+      const int r = (int)c0 + threadIdx.x;
+      if (r < rows) {
+        const float2 v = row_ml(a, pairs, pair, r);
+        lse[threadIdx.x] = v.x + log2_hw(v.y);
+      }
+      __syncthreads();
+      const int end = rows - c0 < kAtThreads ? (int)(rows - c0) : kAtThreads;
+      if (held)
+        for (int k = sub; k < end; k += lanes)
+          if (c0 + k >= r0) w += exp2_hw(from[c0 + k] - lse[k]);
     }
   }
-  for (int x = 1; x < lanes; x <<= 1) w += __shfl_xor(w, x, kWave);
+  for (int x = 1; x < lanes && x < kWave; x <<= 1) w += __shfl_xor(w, x, kWave);
+  if (lanes > kWave) {
+    __shared__ float part[kAtThreads / kWave];
+    if (lane_id() == 0) part[wave_id()] = w;
+    __syncthreads();
+    w = 0.f;
+#pragma unroll
+    for (int i = 0; i < kAtThreads / kWave; ++i) w += part[i];
+  }
   if (sub == 0 && held) a.score[(int64_t)pair * a.max_blocks + b] += w;
 }
 
@@ -779,10 +816,11 @@ hipError_t attend_run(const AttendArgs& a, hipStream_t s) {
     else k_attend<T, D, NB, false><<<grid, kFewThreads, 0, s>>>(a);
   }
   hipError_t e = hipGetLastError();
-  if (e != hipSuccess || (a.splits == 1 && !a.score)) return e;
+  // (k_attend adds up the scores of rows that one workgroup has whole)
+  if (e != hipSuccess || (a.splits == 1 && (!a.score || (!MANY && a.tiles == 1)))) return e;
   const int each = a.splits <= kFewSplits ? kAtThreads / (D / 4) : 1;      // rows of a workgroup
   const int row_groups = a.splits > 1 ? (int)(((int64_t)pairs * a.r_max + each - 1) / each) : 0;
-  const int blocks = kAtThreads / score_lanes(a.r_max);                    // blocks of a workgroup
+  const int blocks = kAtThreads / score_lanes(a.r_max, a.splits);          // blocks of a workgroup
   const int score_groups = a.score ? pairs * ((a.max_nb + blocks - 1) / blocks) : 0;
   k_attend_join<T, D><<<dim3((unsigned)row_groups + score_groups), kAtThreads, 0, s>>>(a, row_groups);
   return hipGetLastError();
@@ -821,7 +859,12 @@ AttendPlan attend_plan(int n_seqs, int hk, int group, int d, int dtype, int max_
   // 8192 tokens, D = 128, 91.9 us without and 96.3 with two; 56 x 4 pairs of
   // 4001 tokens in fp32 38.9 us without and 45.2 with two.
   int64_t splits = 256 / wgs;
-  const int64_t most = (p.max_nb + 7) / 8;
+  // Up to four blocks a wave one launch beats the split and its join: 8 pairs, D =
+  // 128, 400 / 800 / 1000 / 1500 tokens 7.1 / 8.9 / 10.0 / 12.3 us whole and 9.1 /
+  // 9.9 / 10.0 / 10.1 split; with scores and several tiles the join runs anyway
+  // (fp32, 40 rows, 1000 tokens 15.5 and 13.9).
+  const bool whole = !p.many && p.max_nb <= 4 * kFewWaves && (!score || p.tiles == 1);
+  const int64_t most = whole ? 1 : (p.max_nb + 7) / 8;
   splits = splits < most ? splits : most;
   splits = splits < kMaxSplits ? splits : kMaxSplits;
   p.splits = (int)(splits > 1 ? splits : 1);
