@@ -252,8 +252,13 @@ pi_status pi_attend(const pi_kv_cache* cache, const void* q, int64_t q_tok_strid
   a.max_nb = p.max_nb;
   a.tiles = p.tiles;
   a.splits = p.splits;
+  a.slots = p.slots;
+  a.share_even = p.share_even;
+  a.share_safe = p.share_safe;
+  a.splits_max = p.splits_max;
   a.part = reinterpret_cast<float*>(w + p.part);
   a.ml = reinterpret_cast<float2*>(w + p.ml);
+  a.count = reinterpret_cast<int*>(w + p.count);
   a.lse = reinterpret_cast<float*>(w + p.lse);
   a.flags = reinterpret_cast<unsigned*>(w) + PI_WS_FLAGS;
   const hipError_t e = pi::launch_attend(a, p, d, dtype, static_cast<hipStream_t>(stream));

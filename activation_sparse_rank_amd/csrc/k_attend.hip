@@ -113,20 +113,70 @@ __device__ void nan_rows(const AttendArgs& a, const Seq& q, int h, int d, int64_
   }
 }
 
+// How sequences share a.slots workgroups by their lengths: the fewest blocks to
+// a workgroup (of 64 counts between the bounds) that leave no more workgroups than
+// there are.  Lane s has sequence s's.
+struct Shares {
+  Seq q;
+  int n, first;          // workgroups of each of its kv heads; the first of them
+  __device__ Shares(const AttendArgs& a) {
+    const int s = lane_id();
+    q = read_seq(a.lens, a.q_start, s < a.n_seqs ? s : 0, a.max_q, a.n_tok, a.max_len);
+    // One for a sequence that is invalid or without tokens, for its NaN or zeros
+    // (without rows it needs none, but splits_max counts it).
+    int nb = q.n ? (q.len + kBlk - 1) / kBlk : 0;
+    nb = s < a.n_seqs ? (nb > 1 ? nb : 1) : 0;
+    const float sum = (float)__builtin_amdgcn_readlane((int)wave_scan((unsigned)nb), kWave - 1);
+    const float most = (float)__builtin_amdgcn_readlane((int)wave_max((unsigned)nb), kWave - 1);
+    // Between an even share (a block to each wave at least, kMaxSplits at most)
+    // and what is always enough: the longest, and sum / per + n_seqs workgroups.
+    const float lo = fmaxf(fmaxf(sum * a.share_even, most * (1.f / kMaxSplits)), (float)kFewWaves);
+    const float hi = fmaxf(fminf(most, sum * a.share_safe), lo);
+    const float per = s == kWave - 1 ? hi : lo + (hi - lo) * ((float)s * (1.f / (kWave - 1)));
+    const float inv = __builtin_amdgcn_rcpf(per), x = (float)nb - 0.5f;
+    int used = 0;
+    for (int i = 0; i < a.n_seqs; ++i) used += count(lane_f(x, i), inv);
+    const int at = __builtin_ctzll(__ballot(used <= a.slots / a.hk) | 1ull << (kWave - 1));
+    n = s < a.n_seqs ? count(x, lane_f(inv, at)) : 0;
+    first = ((int)wave_scan((unsigned)n) - n) * a.hk;
+  }
+  // ceil(nb / per) of nb - 0.5, which is exact (nb is under 2^20) and clear of whole numbers.
+  __device__ static int count(float x, float inv) { return (int)(x * inv) + 1; }
+};
+
 // What a (sequence, kv head, split) walks, the same for its whole workgroup.
 struct Walk {
-  int pair, s, h, tile, split;
-  Seq q;
+  int pair, s, h, tile, split, splits;
+  Seq q;                 // (without rows where the slot is nobody's)
   int rows, seen0;       // rows of the pair; tokens that its first row sees (may be < 1)
   __device__ Walk(const AttendArgs& a) {
-    const int pairs = a.n_seqs * a.hk;
-    pair = blockIdx.x % pairs;
-    tile = blockIdx.x / pairs % a.tiles;
-    split = blockIdx.x / pairs / a.tiles;
-    s = pair / a.hk, h = pair % a.hk;
-    q = read_seq(a.lens, a.q_start, s, a.max_q, a.n_tok, a.max_len);
+    if (a.slots) {
+      const Shares x(a);
+      const int slot = blockIdx.x;
+      s = __popcll(__ballot(x.first + x.n * a.hk <= slot));
+      const bool used = s < a.n_seqs;
+      s = used ? s : 0;
+      auto of = [&](int v) { return __builtin_amdgcn_readlane(v, s); };
+      q = {of(x.q.q0), used ? of(x.q.n) : 0, of(x.q.len), !used || of(x.q.ok)};
+      splits = used ? of(x.n) : 1;
+      const int k = slot - of(x.first);
+      h = used ? (int)(((float)k + 0.5f) * __builtin_amdgcn_rcpf((float)splits)) : 0;      // k < 256
+      split = k - h * splits, tile = 0;
+      pair = s * a.hk + h;
+      if (used && split == 0 && threadIdx.x == 0) a.count[pair] = splits;
+    } else {
+      const int pairs = a.n_seqs * a.hk;
+      pair = blockIdx.x % pairs;
+      tile = blockIdx.x / pairs % a.tiles;
+      split = blockIdx.x / pairs / a.tiles, splits = a.splits;
+      s = pair / a.hk, h = pair % a.hk;
+      q = read_seq(a.lens, a.q_start, s, a.max_q, a.n_tok, a.max_len);
+    }
     rows = q.n * a.group;
     seen0 = q.len - q.n + 1;
+  }
+  __device__ int64_t part_at(const AttendArgs& a, int r) const {
+    return ((int64_t)split * a.n_seqs * a.hk + pair) * a.r_max + r;
   }
   // Tokens that row r sees.
   __device__ int sees(const AttendArgs& a, int r) const {
@@ -403,7 +453,7 @@ __global__ __launch_bounds__(kFewThreads, 2) void k_attend(AttendArgs a) {
   const int r1 = r0 + 16 * NB < w.rows ? r0 + 16 * NB : w.rows;
   const int kmin = w.sees(a, r0), kmax = w.sees(a, r1 - 1);
   const int nbk = (kmax + kBlk - 1) / kBlk;
-  const int per = (nbk + a.splits - 1) / a.splits;
+  const int per = (nbk + w.splits - 1) / w.splits;
   const int b0 = w.split * per, b1 = b0 + per < nbk ? b0 + per : nbk;
   const int start = b0 + wave;
   const int mine = start < b1 ? (b1 - start + kFewWaves - 1) / kFewWaves : 0;
@@ -487,7 +537,7 @@ __global__ __launch_bounds__(kFewThreads, 2) void k_attend(AttendArgs a) {
 #pragma unroll
       for (int k = 0; k < E; ++k) v[k] = __builtin_fmaf(f, so[y][row][e0 + k], v[k]);
     }
-    const int64_t at = ((int64_t)w.split * a.n_seqs * a.hk + w.pair) * a.r_max + r;
+    const int64_t at = w.part_at(a, r);
     const bool whole = a.splits == 1;
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     T* p = static_cast<T*>(a.out) + w.out_at(a, r) + e0;
@@ -632,7 +682,7 @@ __global__ __launch_bounds__(G * kManyThreads, 2 * G) void k_attend_many(AttendA
     const int r = r0 + nb * 16 + c;
     if (r >= w.rows) continue;
     const bool whole = a.splits == 1;
-    const int64_t at = ((int64_t)w.split * a.n_seqs * a.hk + w.pair) * a.r_max + r;
+    const int64_t at = w.part_at(a, r);
     const float inv = rows.l[nb] == 0.f ? 0.f : 1.f / rows.l[nb];
     T* p = static_cast<T*>(a.out) + w.out_at(a, r) + 4 * g;
 #pragma unroll
@@ -644,10 +694,10 @@ __global__ __launch_bounds__(G * kManyThreads, 2 * G) void k_attend_many(AttendA
   }
 }
 
-// Reference exponent and sum of a row over its splits.
-__device__ __forceinline__ float2 row_ml(const AttendArgs& a, int pairs, int pair, int r) {
+// Reference exponent and sum of a row over its n splits.
+__device__ __forceinline__ float2 row_ml(const AttendArgs& a, int pairs, int pair, int n, int r) {
   float2 v = a.ml[(int64_t)pair * a.r_max + r];
-  for (int i = 1; i < a.splits; ++i) {
+  for (int i = 1; i < n; ++i) {
     const float2 w = a.ml[((int64_t)i * pairs + pair) * a.r_max + r];
     const float top = fmaxf(v.x, w.x);
     v.y = v.y * exp2_hw(v.x - top) + w.y * exp2_hw(w.x - top);
@@ -679,24 +729,33 @@ __global__ __launch_bounds__(kAtThreads) void k_attend_join(AttendArgs a, int ro
       const int pair = (int)(id / a.r_max), r = (int)(id % a.r_max), e = threadIdx.x % L * 4;
       if (pair >= pairs) return;
       const Seq q = read_seq(a.lens, a.q_start, pair / a.hk, a.max_q, a.n_tok, a.max_len);
-      if (!q.ok || r >= q.n * a.group) return;
-      f32x4 x[kFewSplits];
+      f32x4 x[kFewSplits], o = {0.f, 0.f, 0.f, 0.f};
       float2 v[kFewSplits];
-      float top = kNoMax;
+      float top = kNoMax, sum = 0.f;
+      int n = kFewSplits;
+      for (int i = 0; i < n; i += kFewSplits) {
+        // (the first ones on their way before their number is known)
 #pragma unroll
-      for (int k = 0; k < kFewSplits; ++k) {
-        const int64_t at = ((int64_t)(k < a.splits ? k : 0) * pairs + pair) * a.r_max + r;
-        v[k] = a.ml[at];
-        x[k] = *reinterpret_cast<const f32x4*>(a.part + at * D + e);
-        top = fmaxf(top, v[k].x);
-      }
-      f32x4 o = {0.f, 0.f, 0.f, 0.f};
-      float sum = 0.f;
+        for (int k = 0; k < kFewSplits; ++k) {
+          const int64_t at = ((int64_t)(i + k < a.splits_max ? i + k : 0) * pairs + pair) * a.r_max + r;
+          v[k] = a.ml[at];
+          x[k] = *reinterpret_cast<const f32x4*>(a.part + at * D + e);
+        }
+        if (i == 0) {
+          n = a.slots ? a.count[pair] : a.splits;
+          if (!q.ok || r >= q.n * a.group) return;
+        }
+        float to = top;
 #pragma unroll
-      for (int k = 0; k < kFewSplits; ++k) {
-        const float f = k < a.splits ? exp2_hw(v[k].x - top) : 0.f;
-        sum = __builtin_fmaf(f, v[k].y, sum);
-        o += k < a.splits ? f * x[k] : f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int k = 0; k < kFewSplits; ++k) to = i + k < n ? fmaxf(to, v[k].x) : to;
+        const float down = exp2_hw(top - to);
+        top = to, sum *= down, o *= down;
+#pragma unroll
+        for (int k = 0; k < kFewSplits; ++k) {
+          const float f = i + k < n ? exp2_hw(v[k].x - top) : 0.f;
+          sum = i + k < n ? __builtin_fmaf(f, v[k].y, sum) : sum;
+          o += i + k < n ? f * x[k] : f32x4{0.f, 0.f, 0.f, 0.f};
+        }
       }
       const int h = pair % a.hk;
       T* p = static_cast<T*>(a.out) + (int64_t)(q.q0 + r / a.group) * a.o_ts + (int64_t)(h * a.group + r % a.group) * a.o_hs;
@@ -706,18 +765,20 @@ __global__ __launch_bounds__(kAtThreads) void k_attend_join(AttendArgs a, int ro
     __shared__ f32x4 acc[G][L];
     const int pair = blockIdx.x / a.r_max, r = blockIdx.x % a.r_max;
     const Seq q = read_seq(a.lens, a.q_start, pair / a.hk, a.max_q, a.n_tok, a.max_len);
-    if (!q.ok || r >= q.n * a.group) return;
+    const int n = a.slots ? a.count[pair] : a.splits;
+    if (!a.slots && (!q.ok || r >= q.n * a.group)) return;
     // Every split's part of this thread's elements, in flight while the weights are found.
     const int lane = lane_id(), part = threadIdx.x / L, e = threadIdx.x % L * 4;
     constexpr int N = kMaxSplits / G;
     f32x4 x[N];
 #pragma unroll
     for (int k = 0; k < N; ++k) {
-      const int i = k * G + part < a.splits ? k * G + part : 0;
+      const int i = k * G + part < a.splits_max ? k * G + part : 0;
       x[k] = *reinterpret_cast<const f32x4*>(a.part + (((int64_t)i * pairs + pair) * a.r_max + r) * D + e);
     }
-    float2 v = {kNoMax, 0.f};
-    if (lane < a.splits) v = a.ml[((int64_t)lane * pairs + pair) * a.r_max + r];
+    float2 v = a.ml[((int64_t)(lane < a.splits_max ? lane : 0) * pairs + pair) * a.r_max + r];
+    if (a.slots && (!q.ok || r >= q.n * a.group)) return;
+    if (lane >= n) v = {kNoMax, 0.f};
     float top = v.x;
 #pragma unroll
     for (int y = 32; y >= 1; y >>= 1) top = fmaxf(top, __shfl_xor(top, y, kWave));
@@ -728,7 +789,7 @@ __global__ __launch_bounds__(kAtThreads) void k_attend_join(AttendArgs a, int ro
     for (int k = 0; k < N; ++k) {
       const int i = k * G + part;
       const float w = __shfl(f, i, kWave);
-      o += i < a.splits ? w * x[k] : f32x4{0.f, 0.f, 0.f, 0.f};
+      o += i < n ? w * x[k] : f32x4{0.f, 0.f, 0.f, 0.f};
     }
     acc[part][e / 4] = o;
     __syncthreads();
@@ -747,6 +808,8 @@ __global__ __launch_bounds__(kAtThreads) void k_attend_join(AttendArgs a, int ro
   const Seq q = read_seq(a.lens, a.q_start, pair / a.hk, a.max_q, a.n_tok, a.max_len);
   if (!q.ok || first * kBlk >= q.len) return;
   const int rows = q.n * a.group, seen0 = q.len - q.n + 1;
+  if (rows == 0) return;
+  const int splits = a.slots ? a.count[pair] : a.splits;
   const int b = first + threadIdx.x / lanes, sub = threadIdx.x % lanes;
   const bool held = b * kBlk < q.len;
   // The first row that sees a token of block b (the rows after it do too).
@@ -757,7 +820,7 @@ __global__ __launch_bounds__(kAtThreads) void k_attend_join(AttendArgs a, int ro
     if (held && r0 < rows) {
 #pragma unroll 4
       for (int r = (int)r0 + sub; r < rows; r += kAtThreads) {
-        const float2 v = row_ml(a, pairs, pair, r);
+        const float2 v = row_ml(a, pairs, pair, splits, r);
         w += exp2_hw(from[r] - v.x - log2_hw(v.y));
       }
     }
@@ -768,7 +831,7 @@ __global__ __launch_bounds__(kAtThreads) void k_attend_join(AttendArgs a, int ro
       __syncthreads();
       const int r = (int)c0 + threadIdx.x;
       if (r < rows) {
-        const float2 v = row_ml(a, pairs, pair, r);
+        const float2 v = row_ml(a, pairs, pair, splits, r);
         lse[threadIdx.x] = v.x + log2_hw(v.y);
       }
       __syncthreads();
@@ -805,7 +868,7 @@ constexpr int most_rows_few(int d, bool f32) { return f32 ? 256 : 16 * few_tiles
 template <typename T, int D, int NB, bool MANY>
 hipError_t attend_run(const AttendArgs& a, hipStream_t s) {
   const int pairs = a.n_seqs * a.hk;
-  const dim3 grid((unsigned)pairs * a.tiles * a.splits);
+  const dim3 grid((unsigned)(a.slots ? a.slots : pairs * a.tiles * a.splits));
   if constexpr (MANY) {
     // Two groups where the rows' registers leave room for four waves a SIMD.
     constexpr int G = D == 64 && sizeof(T) == 2 ? 2 : 1;
@@ -868,14 +931,33 @@ AttendPlan attend_plan(int n_seqs, int hk, int group, int d, int dtype, int max_
   splits = splits < most ? splits : most;
   splits = splits < kMaxSplits ? splits : kMaxSplits;
   p.splits = (int)(splits > 1 ? splits : 1);
+  p.slots = 0, p.splits_max = p.splits, p.share_even = p.share_safe = 0.f;
+  // Sequences share the workgroups by their lengths where a longest one's splits have
+  // 32 blocks and more: 8 sequences x 8 heads, D = 128, 16000 tokens each 47.5 us
+  // and 46.0 without; 16000 down to 2700 31.9 and 34.2; one of 16000 beside seven of 300
+  // 18.8 and 27.4; under 32 blocks (4 x 8, 2000 tokens and less) 11.1 and 10.2.
+  if (!p.many && p.tiles == 1 && n_seqs > 1 && n_seqs <= kWave && p.splits > 1 && p.max_nb / p.splits >= 32 &&
+      p.max_nb < 1 << 20) {
+    p.slots = 256;
+    const float each = (float)(256 / hk);
+    p.share_even = 1.f / each;
+    p.share_safe = each > n_seqs ? (1.f + 0x1p-16f) / (each - (float)n_seqs) : 1e30f;
+    if (p.splits == 1) p.splits = 2;
+    // one sequence has what the others leave
+    p.splits_max = 256 / hk - (n_seqs - 1);
+    p.splits_max = p.splits_max < kMaxSplits ? p.splits_max : kMaxSplits;
+  }
+  const size_t parts = (size_t)p.splits_max * pairs;
   auto up256 = [](size_t v) { return (v + 255) & ~size_t(255); };
   size_t off = PI_WS_HEADER_BYTES;
   p.part = off;
-  off += up256(p.splits > 1 ? (size_t)p.splits * pairs * p.r_max * d * sizeof(float) : 0);
+  off += up256(p.splits > 1 ? parts * p.r_max * d * sizeof(float) : 0);
   p.ml = off;
-  off += up256(p.splits > 1 || score ? (size_t)p.splits * pairs * p.r_max * sizeof(float2) : 0);
+  off += up256(p.splits > 1 || score ? parts * p.r_max * sizeof(float2) : 0);
   p.lse = off;
   off += up256(score ? (size_t)pairs * p.max_nb * p.r_max * sizeof(float) : 0);
+  p.count = off;
+  off += up256(p.slots ? (size_t)pairs * sizeof(int) : 0);
   p.total = off;
   return p;
 }

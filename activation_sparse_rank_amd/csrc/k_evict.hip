@@ -31,31 +31,6 @@ __device__ __forceinline__ unsigned order_key(float f) {
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
-// Inclusive sums over the lanes of a wave, lane 0 first: shifts inside rows of
-// 16 lanes, then the rows' ends handed on.
-__device__ __forceinline__ unsigned wave_scan(unsigned x) {
-  int v = (int)x;
-  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);   // row_shr:1
-  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);   // row_shr:2
-  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);   // row_shr:4
-  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);   // row_shr:8
-  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);   // row_bcast:15 into rows 1 and 3
-  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);   // row_bcast:31 into rows 2 and 3
-  return (unsigned)v;
-}
-
-// The largest of the lanes' values, in lane 63 (the same steps).
-__device__ __forceinline__ unsigned wave_max(unsigned v) {
-  auto step = [&](unsigned x) { v = v > x ? v : x; };
-  step((unsigned)__builtin_amdgcn_update_dpp(0, (int)v, 0x111, 0xf, 0xf, false));
-  step((unsigned)__builtin_amdgcn_update_dpp(0, (int)v, 0x112, 0xf, 0xf, false));
-  step((unsigned)__builtin_amdgcn_update_dpp(0, (int)v, 0x114, 0xf, 0xf, false));
-  step((unsigned)__builtin_amdgcn_update_dpp(0, (int)v, 0x118, 0xf, 0xf, false));
-  step((unsigned)__builtin_amdgcn_update_dpp(0, (int)v, 0x142, 0xa, 0xf, false));
-  step((unsigned)__builtin_amdgcn_update_dpp(0, (int)v, 0x143, 0xc, 0xf, false));
-  return v;
-}
-
 // How many of keys[0 .. n) go before the key k of number i: larger, or equal
 // with a lower number.  The wave's lanes have the numbers base .. base + 63 and
 // their keys (0 past n); n is a multiple of 4.

@@ -280,10 +280,13 @@ struct AttendPlan {
   int nb;                   // 16-row tiles per wave
   bool many;                // each wave has rows of its own; else the waves of a workgroup share rows and split the blocks
   int tiles;                // workgroups over the rows of a (sequence, kv head)
-  int splits;               // workgroups over the blocks
+  int splits;               // workgroups over the blocks (with slots: on average)
+  int slots;                // workgroups that the sequences share by their lengths; 0: splits each
+  int splits_max;           // of a (sequence, kv head)
+  float share_even, share_safe; // blocks to a workgroup per block of all sequences: evenly, and always enough
   int r_max;                // rows of a (sequence, kv head): max_q * group
   int max_nb;               // blocks of max_len
-  size_t part, ml, lse;     // offsets in the workspace (after its header)
+  size_t part, ml, lse, count;  // offsets in the workspace (after its header)
   size_t total;             // bytes, the header among them
 };
 AttendPlan attend_plan(int n_seqs, int hk, int group, int d, int dtype, int max_q, int max_len, bool score);
@@ -301,10 +304,12 @@ struct AttendArgs {
   float* score;             // nullable: no score
   int n_seqs, hk, group, n_tok, max_q, max_len, max_blocks, n_pages;
   float scale;              // of the logits, times log2(e)
-  int r_max, max_nb, tiles, splits;
-  float* part;              // [splits][n_seqs * hk][r_max][d] sums of a split's weights times values
-  float2* ml;               // [splits][n_seqs * hk][r_max] reference exponent and sum of the weights
+  int r_max, max_nb, tiles, splits, slots, splits_max;
+  float* part;              // [splits_max][n_seqs * hk][r_max][d] sums of a split's weights times values
+  float share_even, share_safe;
+  float2* ml;               // [splits_max][n_seqs * hk][r_max] reference exponent and sum of the weights
   float* lse;               // [n_seqs * hk][max_nb][r_max] log2 of a block's weights
+  int* count;               // [n_seqs * hk] splits (where slots > 0)
   unsigned* flags;
 };
 hipError_t launch_attend(const AttendArgs& a, const AttendPlan& p, int d, int dtype, hipStream_t s);

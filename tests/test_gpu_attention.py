@@ -357,6 +357,60 @@ def test_attend_prompt(dt, d, hk, group, new, length, score):
     _check_attend(c, q, out, ln, qs, d ** -0.5, s0, c.score)
 
 
+def _mixed(seqs, *long):
+    """Long sequences among short ones, some of them empty."""
+    lens = [(13 * i) % 150 if i % 5 else 0 for i in range(seqs)]
+    for i, n in enumerate(long):
+        lens[(7 * i + 3) % seqs] = n
+    return tuple(lens)
+
+
+SHARED = [  # lens, kv heads, group: few rows and more than 32 blocks to a split of the longest
+    (_mixed(40, 4000, 2500), 2, 8),
+    (_mixed(64, 4500), 1, 1),
+    (_mixed(64, 2500, 2100, 1000), 2, 4),
+    ((13000, 40, 9000), 7, 3),
+    ((33000, 32999), 1, 3),
+    ((0, 33000, 0), 1, 2),
+]
+
+
+@pytest.mark.parametrize("dt,d", [(f16, 128), (f16, 64), (f32, 64), (f32, 128)])
+@pytest.mark.parametrize("score", [False, True])
+@pytest.mark.parametrize("case", SHARED, ids=[str(i) for i in range(len(SHARED))])
+def test_attend_sequences_of_unlike_lengths(dt, d, score, case):
+    """Sequences that share the workgroups by their lengths, some without rows, one invalid."""
+    lens, hk, group = case
+    c = _filled(len(lens), hk, d, dt, lens, score=score)
+    new = [0 if i % 11 == 8 else (2 if n > 1 and i % 3 == 1 and group <= 8 else 1) for i, n in enumerate(lens)]
+    n = sum(new)
+    q = (torch.randn((n, hk * group, d), device=DEV, generator=torch.Generator(device=DEV).manual_seed(n)) * 2).to(dt)
+    ln = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    qs = torch.from_numpy(np.concatenate(([0], np.cumsum(new))).astype(np.int32)).to(DEV)
+    s0 = c.score.clone() if score else None
+    out, ws = _attend(c, q, ln, qs, max(new), score)
+    s1 = c.score.clone() if score else None
+    _check_attend(c, q, out, ln, qs, d ** -0.5, s0, s1, [s for s in range(len(lens)) if new[s]])
+    assert pi.read_flags(ws) == 0
+    if score:
+        c.score.copy_(s0)
+    ws[256:].fill_(255)                                          # a used workspace holds anything
+    again, _ = _attend(c, q, ln, qs, max(new), score, ws)
+    assert torch.equal(out, again) and (not score or torch.equal(s1, c.score))
+    # the last sequence invalid: NaN in its rows, the others as they are
+    if score:
+        c.score.copy_(s0)
+    ln[-1] = -1
+    bad, _ = _attend(c, q, ln, qs, max(new), score, ws)
+    assert pi.read_flags(ws) == L.PI_FLAG_KV_RANGE
+    at = int(qs[-2])
+    assert torch.isnan(bad[at:]).all()
+    rest = [s for s in range(len(lens) - 1) if new[s]]
+    _check_attend(c, q, bad, ln, qs, d ** -0.5, s0, c.score, rest)
+    if score:
+        assert torch.equal(c.score[-1], s0[-1])
+
+
 @pytest.mark.parametrize("dt", [f16, f32])
 def test_attend_strided_rows_and_scale(dt):
     lens, hk, group, d = (200, 77), 2, 4, 64
