@@ -44,6 +44,7 @@ constexpr int kFewThreads = 512, kFewWaves = kFewThreads / kWave;
 constexpr int kManyThreads = 512;
 constexpr int kManyWaves = kManyThreads / kWave;
 constexpr int kMaxSplits = 64;
+constexpr int kSlots = 256;                  // workgroups that run at once
 constexpr float kNoMax = -3e38f;     // reference before the first visible token
 // Weights are held times 2^6, and a lane's eight of a block may sum to 2^15
 // (fp16 holds 65504) before the reference moves: no maximum is taken but
@@ -160,7 +161,7 @@ struct Walk {
       q = {of(x.q.q0), used ? of(x.q.n) : 0, of(x.q.len), !used || of(x.q.ok)};
       splits = used ? of(x.n) : 1;
       const int k = slot - of(x.first);
-      h = used ? (int)(((float)k + 0.5f) * __builtin_amdgcn_rcpf((float)splits)) : 0;      // k < 256
+      h = used ? (int)(((float)k + 0.5f) * __builtin_amdgcn_rcpf((float)splits)) : 0;      // k < 2^13
       split = k - h * splits, tile = 0;
       pair = s * a.hk + h;
       if (used && split == 0 && threadIdx.x == 0) a.count[pair] = splits;
@@ -538,7 +539,7 @@ __global__ __launch_bounds__(kFewThreads, 2) void k_attend(AttendArgs a) {
       for (int k = 0; k < E; ++k) v[k] = __builtin_fmaf(f, so[y][row][e0 + k], v[k]);
     }
     const int64_t at = w.part_at(a, r);
-    const bool whole = a.splits == 1;
+    const bool whole = w.splits == 1;
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     T* p = static_cast<T*>(a.out) + w.out_at(a, r) + e0;
 #pragma unroll
@@ -555,7 +556,7 @@ __global__ __launch_bounds__(kFewThreads, 2) void k_attend(AttendArgs a) {
   }
   if constexpr (SCORE) {
     // The blocks' weights are in the workspace, from this workgroup's waves.
-    if (a.splits > 1 || a.tiles > 1) return;
+    if (w.splits > 1 || a.tiles > 1) return;
     __threadfence_block();
     __syncthreads();
     constexpr int Q = 4;                            // lanes that share a block's rows
@@ -733,8 +734,12 @@ __global__ __launch_bounds__(kAtThreads) void k_attend_join(AttendArgs a, int ro
       float2 v[kFewSplits];
       float top = kNoMax, sum = 0.f;
       int n = kFewSplits;
+      if (a.slots > kSlots) {
+        n = a.count[pair];
+        if (n == 1) return;
+      }
       for (int i = 0; i < n; i += kFewSplits) {
-        // (the first ones on their way before their number is known)
+        // (mostly the first ones are on their way before their number is known)
 #pragma unroll
         for (int k = 0; k < kFewSplits; ++k) {
           const int64_t at = ((int64_t)(i + k < a.splits_max ? i + k : 0) * pairs + pair) * a.r_max + r;
@@ -743,7 +748,7 @@ __global__ __launch_bounds__(kAtThreads) void k_attend_join(AttendArgs a, int ro
         }
         if (i == 0) {
           n = a.slots ? a.count[pair] : a.splits;
-          if (!q.ok || r >= q.n * a.group) return;
+          if (!q.ok || r >= q.n * a.group || n == 1) return;
         }
         float to = top;
 #pragma unroll
@@ -777,7 +782,7 @@ __global__ __launch_bounds__(kAtThreads) void k_attend_join(AttendArgs a, int ro
       x[k] = *reinterpret_cast<const f32x4*>(a.part + (((int64_t)i * pairs + pair) * a.r_max + r) * D + e);
     }
     float2 v = a.ml[((int64_t)(lane < a.splits_max ? lane : 0) * pairs + pair) * a.r_max + r];
-    if (a.slots && (!q.ok || r >= q.n * a.group)) return;
+    if (a.slots && (!q.ok || r >= q.n * a.group || n == 1)) return;
     if (lane >= n) v = {kNoMax, 0.f};
     float top = v.x;
 #pragma unroll
@@ -810,6 +815,7 @@ __global__ __launch_bounds__(kAtThreads) void k_attend_join(AttendArgs a, int ro
   const int rows = q.n * a.group, seen0 = q.len - q.n + 1;
   if (rows == 0) return;
   const int splits = a.slots ? a.count[pair] : a.splits;
+  if (a.slots && splits == 1) return;               // k_attend has them whole
   const int b = first + threadIdx.x / lanes, sub = threadIdx.x % lanes;
   const bool held = b * kBlk < q.len;
   // The first row that sees a token of block b (the rows after it do too).
@@ -932,19 +938,24 @@ AttendPlan attend_plan(int n_seqs, int hk, int group, int d, int dtype, int max_
   splits = splits < kMaxSplits ? splits : kMaxSplits;
   p.splits = (int)(splits > 1 ? splits : 1);
   p.slots = 0, p.splits_max = p.splits, p.share_even = p.share_safe = 0.f;
-  // Sequences share the workgroups by their lengths where a longest one's splits have
-  // 32 blocks and more: 8 sequences x 8 heads, D = 128, 16000 tokens each 47.5 us
+  // Sequences share the workgroups by their lengths where the longest may have 32
+  // blocks and more to a split: 8 sequences x 8 heads, D = 128, 16000 tokens each 47.5 us
   // and 46.0 without; 16000 down to 2700 31.9 and 34.2; one of 16000 beside seven of 300
   // 18.8 and 27.4; under 32 blocks (4 x 8, 2000 tokens and less) 11.1 and 10.2.
-  if (!p.many && p.tiles == 1 && n_seqs > 1 && n_seqs <= kWave && p.splits > 1 && p.max_nb / p.splits >= 32 &&
-      p.max_nb < 1 << 20) {
-    p.slots = 256;
-    const float each = (float)(256 / hk);
-    p.share_even = 1.f / each;
+  // Beyond 128 pairs only those are split that have twice the mean of 256 pairs: 32 x
+  // 8 of 16384 168 us and 163 (the join's launch), lengths between 100 and 16384,
+  // the mean a fifth of the longest, 53 and 85; one of 16384 beside 31 of 200 21 and 79.
+  // (Half as much more than the mean: 20 x 8 of 8192 72 us and 58.)
+  const bool spare = p.splits == 1;
+  if (!p.many && p.tiles == 1 && n_seqs > 1 && n_seqs <= kWave && hk <= kWave && p.max_nb < 1 << 20 &&
+      (spare ? p.max_nb >= 8 * 32 : p.max_nb / p.splits >= 32)) {
+    p.slots = kSlots + (spare ? (int)pairs : 0);
+    const float each = (float)(p.slots / hk);
+    p.share_even = (spare ? 2.f : 1.f) / (float)(kSlots / hk);
     p.share_safe = each > n_seqs ? (1.f + 0x1p-16f) / (each - (float)n_seqs) : 1e30f;
-    if (p.splits == 1) p.splits = 2;
+    if (spare) p.splits = 2;
     // one sequence has what the others leave
-    p.splits_max = 256 / hk - (n_seqs - 1);
+    p.splits_max = p.slots / hk - (n_seqs - 1);
     p.splits_max = p.splits_max < kMaxSplits ? p.splits_max : kMaxSplits;
   }
   const size_t parts = (size_t)p.splits_max * pairs;

@@ -372,6 +372,8 @@ SHARED = [  # lens, kv heads, group: few rows and more than 32 blocks to a split
     ((13000, 40, 9000), 7, 3),
     ((33000, 32999), 1, 3),
     ((0, 33000, 0), 1, 2),
+    (_mixed(20, 9000, 5000, 700), 8, 2),                         # more pairs than splits: the long alone are split
+    (_mixed(64, 9000, 2000), 6, 1),
 ]
 
 
