@@ -47,8 +47,8 @@ constexpr int kMaxSplits = 64;
 constexpr int kSlots = 256;                  // workgroups that run at once
 constexpr float kNoMax = -3e38f;     // reference before the first visible token
 // Weights are held times 2^6, and a lane's eight of a block may sum to 2^15
-// (fp16 holds 65504) before the reference moves: no maximum is taken but
-// then.  What a weight loses below fp16's smallest step is at most 2^-31 of the
+// (the row's 32, where they are summed, to 2^16; fp16 holds 65504, what is beyond
+// sums to infinity) before the reference moves: no maximum is taken but then.  What a weight loses below fp16's smallest step is at most 2^-31 of the
 // row's largest weight, so that 10^5 such tokens beside one that takes the
 // row are still counted.
 constexpr float kBias = 6.f;
@@ -150,8 +150,8 @@ struct Walk {
   int pair, s, h, tile, split, splits;
   Seq q;                 // (without rows where the slot is nobody's)
   int rows, seen0;       // rows of the pair; tokens that its first row sees (may be < 1)
-  __device__ Walk(const AttendArgs& a) {
-    if (a.slots) {
+  __device__ __forceinline__ Walk(const AttendArgs& a, bool shared) {
+    if (shared) {
       const Shares x(a);
       const int slot = blockIdx.x;
       s = __popcll(__ballot(x.first + x.n * a.hk <= slot));
@@ -372,20 +372,17 @@ struct Rows {
       if constexpr (TWOP || SCORE) {
         sum[nb] = (p[0] + p[1] + (p[2] + p[3])) + (p[4] + p[5] + (p[6] + p[7]));
       } else {
-        // the sum of the rounded weights, which the second product multiplies
-        const u32x4 v = __builtin_bit_cast(u32x4, pf[nb]);
-        const f16x2 one = {(f16)1.f, (f16)1.f};
-        float y = __builtin_amdgcn_fdot2(as_h2(v.x), one, 0.f, false);
-        y = __builtin_amdgcn_fdot2(as_h2(v.y), one, y, false);
-        y = __builtin_amdgcn_fdot2(as_h2(v.z), one, y, false);
-        sum[nb] = __builtin_amdgcn_fdot2(as_h2(v.w), one, y, false);
+        // the sum of the rounded weights over the row, by a product with ones (four
+        // additions by pairs and the lanes' sum at the end: 160 us for 158, 512-token chunk)
+        const f16x8 ones = {(f16)1.f, (f16)1.f, (f16)1.f, (f16)1.f, (f16)1.f, (f16)1.f, (f16)1.f, (f16)1.f};
+        sum[nb] = mfma16(ones, pf[nb], f32x4{0.f, 0.f, 0.f, 0.f})[0];
       }
     };
     bool over = false;
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
       weights(nb);
-      over |= !(sum[nb] < kMost);
+      over |= !(sum[nb] < (TWOP || SCORE ? kMost : 2.f * kMost));
     }
     if (__any(over)) {                             // a weight passes the reference by too much: move it
 #pragma unroll
@@ -427,7 +424,8 @@ struct Rows {
 
   __device__ __forceinline__ void finish() {
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb) l[nb] = row_sum(l[nb]);
+    for (int nb = 0; nb < NB; ++nb)
+      if constexpr (TWOP || SCORE) l[nb] = row_sum(l[nb]);
     rescale(vref);
   }
 };
@@ -442,7 +440,7 @@ __device__ __forceinline__ void store4(T* p, f32x4 v) {
 template <typename T, int D, int NB, bool SCORE>
 __global__ __launch_bounds__(kFewThreads, 2) void k_attend(AttendArgs a) {
   constexpr int KK = D / 64, DT = D / 16, DB = D / 32;
-  const Walk w(a);
+  const Walk w(a, a.slots != 0);
   const int lane = lane_id(), wave = wave_id(), g = lane / 16, c = lane % 16;
   if (!w.q.ok) {
     if (w.split == 0) nan_rows<T>(a, w.q, w.h, D, (int64_t)w.tile * kFewThreads + threadIdx.x, (int64_t)a.tiles * kFewThreads);
@@ -581,7 +579,7 @@ template <typename T, int D, int NB, bool SCORE, int G>
 __global__ __launch_bounds__(G * kManyThreads, 2 * G) void k_attend_many(AttendArgs a) {
   constexpr int KK = D / 64, DT = D / 16, kUnits = D / 16, kPart = kManyWaves / kUnits, kStep = G * kPart;
   constexpr int kThreads = G * kManyThreads;
-  const Walk w(a);
+  const Walk w(a, false);
   const int lane = lane_id(), g = lane / 16, c = lane % 16;
   const int wave = wave_id() % kManyWaves, group = wave_id() / kManyWaves;
   if (!w.q.ok) {
