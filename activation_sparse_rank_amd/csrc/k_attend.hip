@@ -47,10 +47,11 @@ constexpr int kMaxSplits = 64;
 constexpr int kSlots = 256;                  // workgroups that run at once
 constexpr float kNoMax = -3e38f;     // reference before the first visible token
 // Weights are held times 2^6, and a lane's eight of a block may sum to 2^15
-// (the row's 32, where they are summed, to 2^16; fp16 holds 65504, what is beyond
-// sums to infinity) before the reference moves: no maximum is taken but then.  What a weight loses below fp16's smallest step is at most 2^-31 of the
-// row's largest weight, so that 10^5 such tokens beside one that takes the
-// row are still counted.
+// (the row's 32, where they are summed, to 2^16; fp16 holds 65504, what is
+// beyond sums to infinity) before the reference moves: no maximum is taken but
+// then.  What a weight loses below fp16's smallest step is at most 2^-31 of the
+// row's largest weight, so that 10^5 such tokens beside one that takes the row
+// are still counted.
 constexpr float kBias = 6.f;
 constexpr float kMost = 0x1p15f;
 // Under this share of the wave's largest value scale a block's weights would
@@ -609,7 +610,7 @@ __global__ __launch_bounds__(G * kManyThreads, 2 * G) void k_attend_many(AttendA
   for (int base = b0; base < b1; base += kWave) {
     const int cnt = b1 - base < kWave ? b1 - base : kWave;
     x.find(a, w.pair, base, 1, cnt, bad);
-    auto fetch = [&](int i) {                        // of the step that begins with block i (past cnt: page 0, not used)
+    auto fetch = [&](int i) {                        // of the step that begins with block i (past cnt: any page, not used)
       return ld16(a.pages + (int64_t)__builtin_amdgcn_readlane(x.page, i + sj) * (2 * kBlk * D) + su * 1024 + lane * 16);
     };
     auto turn = [&](int buf, u32x4 v) {
@@ -624,8 +625,8 @@ __global__ __launch_bounds__(G * kManyThreads, 2 * G) void k_attend_many(AttendA
     __syncthreads();
     int buf = 0;
     for (int i = 0; i < cnt; i += kStep) {
-      const bool more = i + kStep < cnt;
-      if (more) next = fetch(i + kStep);
+      // (past cnt too: a condition costs more than the last one's load, 158 us for 156 of a 512-token chunk)
+      next = fetch(i + kStep);
 #pragma unroll
       for (int y = 0; y < kPart; ++y) {
         const int j = group * kPart + y, b = base + i + j;
@@ -640,7 +641,7 @@ __global__ __launch_bounds__(G * kManyThreads, 2 * G) void k_attend_many(AttendA
               [&](int t) { return vals[t]; });
       }
       buf ^= 1;
-      if (more) turn(buf, next);
+      turn(buf, next);
       __syncthreads();                               // this step's operands are free, the next one's there
     }
   }
@@ -897,8 +898,7 @@ template <typename T, int D>
 hipError_t attend_nb(const AttendArgs& a, const AttendPlan& p, hipStream_t s) {
   constexpr bool f32 = sizeof(T) == 4;
   if (p.many) {
-    // (fp32 rows come here in such numbers that they fill the wider tiles)
-    if constexpr (!f32)
+    if constexpr (many_tiles(D, f32) == 2)
       if (p.nb == 1) return attend_run<T, D, 1, true>(a, s);
     return attend_run<T, D, many_tiles(D, f32), true>(a, s);
   }
@@ -919,6 +919,10 @@ AttendPlan attend_plan(int n_seqs, int hk, int group, int d, int dtype, int max_
   // One tile a wave while that is enough: more waves share the rows.
   const int narrow = p.many ? 16 * kManyWaves : 16;
   p.nb = p.r_max <= narrow ? 1 : (p.many ? many_tiles(d, f32) : few_tiles(d));
+  // Small calls (tiles times shares of eight blocks) stay with one: 100 of 1000
+  // tokens, 32 heads, 8 of kv, D = 128 17.7 us and 22.3 with two; 200 of 3000, 32 and 8, D = 64 20.8 and 24.9;
+  // 200 of 8000, 64 and 8, D = 64 57.2 and 52.1.
+  if (p.many && pairs * ((p.r_max + narrow - 1) / narrow) * ((p.max_nb + 7) / 8) <= 1024) p.nb = 1;
   const int wg_rows = narrow * p.nb;
   p.tiles = (p.r_max + wg_rows - 1) / wg_rows;
   const int64_t wgs = pairs * p.tiles;
