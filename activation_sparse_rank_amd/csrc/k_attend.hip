@@ -19,7 +19,8 @@
 // pages' bytes bound the time; the eight waves of a workgroup share the rows
 // and take every eighth block.  Many rows (k_attend_many): the weights' exponentials and the
 // products do; each wave has rows of its own and all walk the blocks in
-// step, whose codes are turned to fp16 once for the workgroup, in LDS.  Both
+// step, whose codes are turned to fp16 once for the workgroup, in LDS (groups of
+// waves take different blocks where the rows leave waves over).  Both
 // split the blocks over workgroups as well where the rows do not fill the
 // CUs; partial sums are joined in a fixed order (in LDS, then in k_attend_join).
 //
@@ -458,8 +459,9 @@ __global__ __launch_bounds__(kFewThreads, 2) void k_attend(AttendArgs a) {
   const int start = b0 + wave;
   const int mine = start < b1 ? (b1 - start + kFewWaves - 1) / kFewWaves : 0;
 
-  // The weights as two parts: the products have time while the pages come.
-  Rows<T, D, NB, SCORE, true> rows;
+  // The weights as two parts: the products have time while the pages come.  (As one
+  // where two tiles of D = 128 would spill: 80 us for 32 x 8 pairs of 4000 tokens, 24 rows, 46.5 so.)
+  Rows<T, D, NB, SCORE, sizeof(T) == 4 || !(D == 128 && NB == 2)> rows;
   rows.load(a, w, r0);
   u32x4 rk[2 * KK], rv[DB];                         // a block's codes, as they lie in the page
   bool bad = false;
@@ -572,23 +574,23 @@ __global__ __launch_bounds__(kFewThreads, 2) void k_attend(AttendArgs a) {
   }
 }
 
-// NB * 16 rows to a wave, kManyWaves waves to a group; the G groups share the
-// rows and take every G-th step.  The codes of a step's blocks become fp16
-// operands in LDS once for all of them: a wave turns one unit (1 KB of a page)
+// NB * 16 rows to a wave, W waves to a group; the G groups share the rows and
+// take blocks of their own in each step.  The codes of a step's blocks become
+// fp16 operands in LDS once for all of them: a wave turns U units (1 KB of a page)
 // per step, and the next step's units are on their way meanwhile.
-template <typename T, int D, int NB, bool SCORE, int G>
-__global__ __launch_bounds__(G * kManyThreads, 2 * G) void k_attend_many(AttendArgs a) {
-  constexpr int KK = D / 64, DT = D / 16, kUnits = D / 16, kPart = kManyWaves / kUnits, kStep = G * kPart;
-  constexpr int kThreads = G * kManyThreads;
+template <typename T, int D, int NB, bool SCORE, int W, int G>
+__global__ __launch_bounds__(W * G * kWave, W * G / 4) void k_attend_many(AttendArgs a) {
+  constexpr int KK = D / 64, DT = D / 16, kUnits = D / 16, kPart = W > kUnits ? W / kUnits : 1, kStep = G * kPart;
+  constexpr int kThreads = W * G * kWave, U = kStep * kUnits / (W * G);       // units that a wave turns
   const Walk w(a, false);
   const int lane = lane_id(), g = lane / 16, c = lane % 16;
-  const int wave = wave_id() % kManyWaves, group = wave_id() / kManyWaves;
+  const int wave = wave_id() % W, group = wave_id() / W;
   if (!w.q.ok) {
     if (w.split == 0) nan_rows<T>(a, w.q, w.h, D, (int64_t)w.tile * kThreads + threadIdx.x, (int64_t)a.tiles * kThreads);
     if (threadIdx.x == 0) raise_flag(a.flags, PI_FLAG_KV_RANGE);
     return;
   }
-  constexpr int kRows = 16 * NB * kManyWaves;
+  constexpr int kRows = 16 * NB * W;
   // The last rows see the most: they begin first.
   const int g0 = (a.tiles - 1 - w.tile) * kRows;
   if (g0 >= w.rows) return;
@@ -606,27 +608,37 @@ __global__ __launch_bounds__(G * kManyThreads, 2 * G) void k_attend_many(AttendA
   rows.load(a, w, r0);
   bool bad = false;
   Blocks x;
-  const int sj = wave_id() / kUnits, su = wave_id() % kUnits; // the unit that this wave turns
   for (int base = b0; base < b1; base += kWave) {
     const int cnt = b1 - base < kWave ? b1 - base : kWave;
     x.find(a, w.pair, base, 1, cnt, bad);
+    u32x4 next[U];
     auto fetch = [&](int i) {                        // of the step that begins with block i (past cnt: any page, not used)
-      return ld16(a.pages + (int64_t)__builtin_amdgcn_readlane(x.page, i + sj) * (2 * kBlk * D) + su * 1024 + lane * 16);
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        const int u = wave_id() * U + k;
+        const int64_t page = __builtin_amdgcn_readlane(x.page, i + u / kUnits);
+        next[k] = ld16(a.pages + page * (2 * kBlk * D) + u % kUnits * 1024 + lane * 16);
+      }
     };
-    auto turn = [&](int buf, u32x4 v) {
-      ops[buf][sj][su][0][lane] = __builtin_bit_cast(u32x4, codes_f16(v.x, v.y));
-      ops[buf][sj][su][1][lane] = __builtin_bit_cast(u32x4, codes_f16(v.z, v.w));
+    auto turn = [&](int buf) {
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        const int u = wave_id() * U + k;
+        const u32x4 v = next[k];
+        ops[buf][u / kUnits][u % kUnits][0][lane] = __builtin_bit_cast(u32x4, codes_f16(v.x, v.y));
+        ops[buf][u / kUnits][u % kUnits][1][lane] = __builtin_bit_cast(u32x4, codes_f16(v.z, v.w));
+      }
     };
-    u32x4 next = fetch(0);
+    fetch(0);
     float vs;
     rows.raise_unit(x.read_scales(a, cnt, vs));
     x.set_units(vs, rows.vref);
-    turn(0, next);
+    turn(0);
     __syncthreads();
     int buf = 0;
     for (int i = 0; i < cnt; i += kStep) {
       // (past cnt too: a condition costs more than the last one's load, 158 us for 156 of a 512-token chunk)
-      next = fetch(i + kStep);
+      fetch(i + kStep);
 #pragma unroll
       for (int y = 0; y < kPart; ++y) {
         const int j = group * kPart + y, b = base + i + j;
@@ -641,7 +653,7 @@ __global__ __launch_bounds__(G * kManyThreads, 2 * G) void k_attend_many(AttendA
               [&](int t) { return vals[t]; });
       }
       buf ^= 1;
-      turn(buf, next);
+      turn(buf);
       __syncthreads();                               // this step's operands are free, the next one's there
     }
   }
@@ -649,8 +661,8 @@ __global__ __launch_bounds__(G * kManyThreads, 2 * G) void k_attend_many(AttendA
   rows.finish();
   if constexpr (G > 1) {
     // The groups' sums, in the order of the groups; a lane's elements are the same in each.
-    __shared__ float2 sml[kManyWaves][NB][kWave];
-    static_assert(sizeof(ops) >= sizeof(f32x4) * kManyWaves * NB * DT * kWave, "a group's sums fit the operands' place");
+    __shared__ float2 sml[W][NB][kWave];
+    static_assert(sizeof(ops) >= sizeof(f32x4) * W * NB * DT * kWave, "a group's sums fit the operands' place");
     f32x4* so = &reinterpret_cast<f32x4*>(ops)[(wave * NB * DT) * kWave + lane];
     for (int y = 1; y < G; ++y) {
       if (group == y) {
@@ -859,26 +871,31 @@ __global__ __launch_bounds__(kAtThreads) void k_attend_join(AttendArgs a, int ro
 }
 
 // 16-row tiles of a wave: what its registers hold, beside the pages' codes in k_attend.
-constexpr int few_tiles(int d) { return d == 64 ? 2 : 1; }
+constexpr int few_tiles(int d, bool f32) { return d == 64 || !f32 ? 2 : 1; }
 constexpr int many_tiles(int d, bool f32) { return d == 128 && f32 ? 1 : 2; }
 
 // k_attend up to so many rows, k_attend_many beyond.  Measured on one card: fp16, D =
-// 128, 4 sequences of 8192 tokens, 32 rows 45.5 us here (two tiles a wave) and
-// 27.3 there; D = 64, 32 rows over 8000 tokens 12.2 and 15.7 us, 64 rows 25.9
+// 128, 32 x 8 pairs of 4000 tokens, 24 rows 46.5 us here and 58 there (four groups of
+// two waves); D = 64, 32 rows over 8000 tokens 12.2 and 15.7 us, 64 rows 25.9
 // and 14.7; fp32 (twice the products either way), D = 64, 128 rows 16.6 and
 // 20.1, 256 rows 17.7 and 27.8, 512 rows 34.4 and 30.5.
-constexpr int most_rows_few(int d, bool f32) { return f32 ? 256 : 16 * few_tiles(d); }
+constexpr int most_rows_few(int d, bool f32) { return f32 ? 256 : 16 * few_tiles(d, f32); }
 
 // Launches one of the two kernels and the join.
-template <typename T, int D, int NB, bool MANY>
+template <typename T, int D, int NB, bool MANY, int W = kManyWaves>
 hipError_t attend_run(const AttendArgs& a, hipStream_t s) {
   const int pairs = a.n_seqs * a.hk;
   const dim3 grid((unsigned)(a.slots ? a.slots : pairs * a.tiles * a.splits));
   if constexpr (MANY) {
     // Two groups where the rows' registers leave room for four waves a SIMD.
     constexpr int G = D == 64 && sizeof(T) == 2 ? 2 : 1;
-    if (a.score) k_attend_many<T, D, NB, true, 1><<<grid, kManyThreads, 0, s>>>(a);
-    else k_attend_many<T, D, NB, false, G><<<grid, G * kManyThreads, 0, s>>>(a);
+    if constexpr (W < kManyWaves) {
+      if (a.score) k_attend_many<T, D, NB, true, W, kManyWaves / W><<<grid, kManyThreads, 0, s>>>(a);
+      else k_attend_many<T, D, NB, false, W, kManyWaves / W><<<grid, kManyThreads, 0, s>>>(a);
+    } else {
+      if (a.score) k_attend_many<T, D, NB, true, W, 1><<<grid, kManyThreads, 0, s>>>(a);
+      else k_attend_many<T, D, NB, false, W, G><<<grid, G * kManyThreads, 0, s>>>(a);
+    }
   } else {
     if (a.score) k_attend<T, D, NB, true><<<grid, kFewThreads, 0, s>>>(a);
     else k_attend<T, D, NB, false><<<grid, kFewThreads, 0, s>>>(a);
@@ -898,11 +915,15 @@ template <typename T, int D>
 hipError_t attend_nb(const AttendArgs& a, const AttendPlan& p, hipStream_t s) {
   constexpr bool f32 = sizeof(T) == 4;
   if (p.many) {
+    if constexpr (!f32) {
+      if (p.waves == 2) return attend_run<T, D, 2, true, 2>(a, s);
+      if (p.waves == 4) return attend_run<T, D, 2, true, 4>(a, s);
+    }
     if constexpr (many_tiles(D, f32) == 2)
       if (p.nb == 1) return attend_run<T, D, 1, true>(a, s);
     return attend_run<T, D, many_tiles(D, f32), true>(a, s);
   }
-  if constexpr (few_tiles(D) == 2)
+  if constexpr (few_tiles(D, f32) == 2)
     if (p.nb == 2) return attend_run<T, D, 2, false>(a, s);
   return attend_run<T, D, 1, false>(a, s);
 }
@@ -916,13 +937,22 @@ AttendPlan attend_plan(int n_seqs, int hk, int group, int d, int dtype, int max_
   p.max_nb = (max_len + kBlk - 1) / kBlk;
   const bool f32 = dtype == PI_F32;
   p.many = p.r_max > most_rows_few(d, f32);
-  // One tile a wave while that is enough: more waves share the rows.
-  const int narrow = p.many ? 16 * kManyWaves : 16;
-  p.nb = p.r_max <= narrow ? 1 : (p.many ? many_tiles(d, f32) : few_tiles(d));
-  // Small calls (tiles times shares of eight blocks) stay with one: 100 of 1000
-  // tokens, 32 heads, 8 of kv, D = 128 17.7 us and 22.3 with two; 200 of 3000, 32 and 8, D = 64 20.8 and 24.9;
-  // 200 of 8000, 64 and 8, D = 64 57.2 and 52.1.
-  if (p.many && pairs * ((p.r_max + narrow - 1) / narrow) * ((p.max_nb + 7) / 8) <= 1024) p.nb = 1;
+  const int64_t shares = pairs * ((p.max_nb + 7) / 8);
+  // Up to 128 rows two or four waves have two tiles each, and the other waves other
+  // blocks: fewer waves read a block's operands (D = 128, 32 x 8 pairs of 4000
+  // tokens: 40 rows 64 us, 72 with one tile and twice the waves, 104 with eight waves
+  // at the same block; 72 rows 80, 107).  Not in small calls (8 pairs of 1500, 40
+  // rows: 15.1 and 13.6) nor for D = 64 (32 x 8 pairs, 72 rows: 59 and 52).
+  p.waves = !p.many ? 1 : kManyWaves;
+  if (p.many && !f32 && d == 128 && shares > 256) p.waves = p.r_max <= 64 ? 2 : p.r_max <= 128 ? 4 : kManyWaves;
+  // Else one tile a wave while that is enough, and in calls that are small (the
+  // workgroups and their shares of eight blocks): 100 of 1000 tokens, 32 heads, 8 of
+  // kv, D = 128 17.7 us and 22.3 with two; 200 of 3000, 32 and 8, D = 64 20.8 and
+  // 24.9; 200 of 8000, 64 and 8, D = 64 57.2 and 52.1.
+  const int narrow = 16 * p.waves, most_tiles = p.many ? many_tiles(d, f32) : few_tiles(d, f32);
+  if (p.many && p.waves < kManyWaves) p.nb = 2;
+  else if (p.many) p.nb = p.r_max <= narrow || shares * ((p.r_max + narrow - 1) / narrow) <= 1024 ? 1 : most_tiles;
+  else p.nb = p.r_max <= narrow ? 1 : most_tiles;
   const int wg_rows = narrow * p.nb;
   p.tiles = (p.r_max + wg_rows - 1) / wg_rows;
   const int64_t wgs = pairs * p.tiles;

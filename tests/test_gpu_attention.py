@@ -413,6 +413,29 @@ def test_attend_sequences_of_unlike_lengths(dt, d, score, case):
         assert torch.equal(c.score[-1], s0[-1])
 
 
+@pytest.mark.parametrize("dt,d", [(f16, 128), (f16, 64), (f32, 64)])
+@pytest.mark.parametrize("score", [False, True])
+@pytest.mark.parametrize("new,group", [(3, 7), (4, 8), (5, 8), (8, 8), (13, 5), (16, 8), (17, 8), (200, 2)])
+def test_attend_a_few_tokens_over_long_contexts(dt, d, score, new, group):
+    """Rows between one token's and a prompt's, ragged, one sequence with fewer of them than the others."""
+    lens, hk = (2200, 2111, 700, 90), 8
+    c = _filled(4, hk, d, dt, lens, score=score)
+    rows = [new, new, 1, min(new, 90)]
+    n = sum(rows)
+    q = (torch.randn((n, hk * group, d), device=DEV, generator=torch.Generator(device=DEV).manual_seed(n)) * 2).to(dt)
+    ln = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    qs = torch.from_numpy(np.concatenate(([0], np.cumsum(rows))).astype(np.int32)).to(DEV)
+    s0 = c.score.clone() if score else None
+    out, ws = _attend(c, q, ln, qs, new, score)
+    _check_attend(c, q, out, ln, qs, d ** -0.5, s0, c.score)
+    assert pi.read_flags(ws) == 0
+    s1 = c.score.clone() if score else None
+    if score:
+        c.score.copy_(s0)
+    again, _ = _attend(c, q, ln, qs, new, score, ws)
+    assert torch.equal(out, again) and (not score or torch.equal(s1, c.score))
+
+
 @pytest.mark.parametrize("dt", [f16, f32])
 def test_attend_strided_rows_and_scale(dt):
     lens, hk, group, d = (200, 77), 2, 4, 64
