@@ -874,13 +874,6 @@ __global__ __launch_bounds__(kAtThreads) void k_attend_join(AttendArgs a, int ro
 constexpr int few_tiles(int d, bool f32) { return d == 64 || !f32 ? 2 : 1; }
 constexpr int many_tiles(int d, bool f32) { return d == 128 && f32 ? 1 : 2; }
 
-// k_attend up to so many rows, k_attend_many beyond.  Measured on one card: fp16, D =
-// 128, 32 x 8 pairs of 4000 tokens, 24 rows 46.5 us here and 58 there (four groups of
-// two waves); D = 64, 32 rows over 8000 tokens 12.2 and 15.7 us, 64 rows 25.9
-// and 14.7; fp32 (twice the products either way), D = 64, 128 rows 16.6 and
-// 20.1, 256 rows 17.7 and 27.8, 512 rows 34.4 and 30.5.
-constexpr int most_rows_few(int d, bool f32) { return f32 ? 256 : 16 * few_tiles(d, f32); }
-
 // Launches one of the two kernels and the join.
 template <typename T, int D, int NB, bool MANY, int W = kManyWaves>
 hipError_t attend_run(const AttendArgs& a, hipStream_t s) {
@@ -915,9 +908,9 @@ template <typename T, int D>
 hipError_t attend_nb(const AttendArgs& a, const AttendPlan& p, hipStream_t s) {
   constexpr bool f32 = sizeof(T) == 4;
   if (p.many) {
-    if constexpr (!f32) {
-      if (p.waves == 2) return attend_run<T, D, 2, true, 2>(a, s);
-      if (p.waves == 4) return attend_run<T, D, 2, true, 4>(a, s);
+    if constexpr (f32 || D == 128) {
+      if (p.waves == 2) return attend_run<T, D, many_tiles(D, f32), true, 2>(a, s);
+      if (p.waves == 4) return attend_run<T, D, many_tiles(D, f32), true, 4>(a, s);
     }
     if constexpr (many_tiles(D, f32) == 2)
       if (p.nb == 1) return attend_run<T, D, 1, true>(a, s);
@@ -936,21 +929,30 @@ AttendPlan attend_plan(int n_seqs, int hk, int group, int d, int dtype, int max_
   p.r_max = max_q * group;
   p.max_nb = (max_len + kBlk - 1) / kBlk;
   const bool f32 = dtype == PI_F32;
-  p.many = p.r_max > most_rows_few(d, f32);
+  // k_attend for the rows of one workgroup: fp16, D = 128, 32 x 8 pairs of 4000
+  // tokens, 24 rows 46.5 us and 58 in k_attend_many; D = 64, 32 rows over 8000
+  // tokens 12.2 and 15.7 us, 64 rows 25.9 and 14.7.  In fp32, whose products are
+  // twice as many, also for a few workgroups that read the same pages: 8 pairs of
+  // 30000 tokens, D = 128, 64 rows 30.7 and 38.2, 256 rows 85 and 77 (of 1500
+  // tokens 15.1 and 21.4); but 32 x 8 pairs of 4000, 64 rows 177 and 88.
+  const int few_rows = 16 * few_tiles(d, f32);
+  p.many = p.r_max > few_rows && (!f32 || p.r_max > 256 || pairs * ((p.r_max + few_rows - 1) / few_rows) > 128);
   const int64_t shares = pairs * ((p.max_nb + 7) / 8);
-  // Up to 128 rows two or four waves have two tiles each, and the other waves other
-  // blocks: fewer waves read a block's operands (D = 128, 32 x 8 pairs of 4000
-  // tokens: 40 rows 64 us, 72 with one tile and twice the waves, 104 with eight waves
-  // at the same block; 72 rows 80, 107).  Not in small calls (8 pairs of 1500, 40
-  // rows: 15.1 and 13.6) nor for D = 64 (32 x 8 pairs, 72 rows: 59 and 52).
+  // Few enough rows for two or four waves leave the others for other blocks, and
+  // fewer waves read a block's operands (32 x 8 pairs of 4000 tokens: fp16, D = 128,
+  // 40 rows 64 us, 72 with one tile and twice the waves, 104 with eight waves at the
+  // same block; 72 rows 80, 107; fp32, D = 128, 24 rows 63.5, 108, D = 64, 64 rows 54.7,
+  // 72.5).  Not in small calls (fp16, 8 pairs of 1500, 40 rows: 15.1 and 13.6) nor for
+  // fp16 of D = 64 (72 rows: 59 and 52).
   p.waves = !p.many ? 1 : kManyWaves;
-  if (p.many && !f32 && d == 128 && shares > 256) p.waves = p.r_max <= 64 ? 2 : p.r_max <= 128 ? 4 : kManyWaves;
-  // Else one tile a wave while that is enough, and in calls that are small (the
-  // workgroups and their shares of eight blocks): 100 of 1000 tokens, 32 heads, 8 of
-  // kv, D = 128 17.7 us and 22.3 with two; 200 of 3000, 32 and 8, D = 64 20.8 and
-  // 24.9; 200 of 8000, 64 and 8, D = 64 57.2 and 52.1.
+  const int two = 32 * many_tiles(d, f32);             // rows of two waves
+  if (p.many && (f32 || d == 128) && shares > 256) p.waves = p.r_max <= two ? 2 : p.r_max <= 2 * two ? 4 : kManyWaves;
+  // Else one tile a wave while that is enough, and in small calls (counted in
+  // shares of eight blocks): 100 of 1000 tokens, 32 heads, 8 of kv, D = 128 17.7 us
+  // and 22.3 with two; 200 of 3000, 32 and 8, D = 64 20.8 and 24.9; 200 of 8000, 64
+  // and 8, D = 64 57.2 and 52.1.
   const int narrow = 16 * p.waves, most_tiles = p.many ? many_tiles(d, f32) : few_tiles(d, f32);
-  if (p.many && p.waves < kManyWaves) p.nb = 2;
+  if (p.many && p.waves < kManyWaves) p.nb = most_tiles;
   else if (p.many) p.nb = p.r_max <= narrow || shares * ((p.r_max + narrow - 1) / narrow) <= 1024 ? 1 : most_tiles;
   else p.nb = p.r_max <= narrow ? 1 : most_tiles;
   const int wg_rows = narrow * p.nb;

@@ -418,9 +418,21 @@ def test_attend_sequences_of_unlike_lengths(dt, d, score, case):
 @pytest.mark.parametrize("new,group", [(3, 7), (4, 8), (5, 8), (8, 8), (13, 5), (16, 8), (17, 8), (200, 2)])
 def test_attend_a_few_tokens_over_long_contexts(dt, d, score, new, group):
     """Rows between one token's and a prompt's, ragged, one sequence with fewer of them than the others."""
-    lens, hk = (2200, 2111, 700, 90), 8
-    c = _filled(4, hk, d, dt, lens, score=score)
-    rows = [new, new, 1, min(new, 90)]
+    _few_tokens((2200, 2111, 700, 90), dt, d, score, new, group)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("score", [False, True])
+@pytest.mark.parametrize("new,group", [(3, 7), (5, 8), (13, 5)])
+def test_attend_a_few_tokens_of_many_sequences(d, score, new, group):
+    _few_tokens((900, 30, 880, 33, 64, 500, 1, 871, 95), f32, d, score, new, group)
+
+
+def _few_tokens(lens, dt, d, score, new, group):
+    hk = 8
+    c = _filled(len(lens), hk, d, dt, lens, score=score)
+    rows = [min(new, x) for x in lens]
+    rows[2] = 1
     n = sum(rows)
     q = (torch.randn((n, hk * group, d), device=DEV, generator=torch.Generator(device=DEV).manual_seed(n)) * 2).to(dt)
     ln = torch.tensor(lens, dtype=torch.int32, device=DEV)
