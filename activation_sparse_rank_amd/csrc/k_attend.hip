@@ -578,8 +578,11 @@ __global__ __launch_bounds__(kFewThreads, 2) void k_attend(AttendArgs a) {
 // take blocks of their own in each step.  The codes of a step's blocks become
 // fp16 operands in LDS once for all of them: a wave turns U units (1 KB of a page)
 // per step, and the next step's units are on their way meanwhile.
+// Waves to a SIMD: those of a workgroup, or two workgroups' where the registers last for them.
+template <typename T, int D, bool SCORE>
+constexpr int many_waves(int waves) { return D == 64 && sizeof(T) == 2 && !SCORE && waves == 8 ? 4 : waves / 4; }
 template <typename T, int D, int NB, bool SCORE, int W, int G>
-__global__ __launch_bounds__(W * G * kWave, W * G / 4) void k_attend_many(AttendArgs a) {
+__global__ __launch_bounds__(W * G * kWave, (many_waves<T, D, SCORE>(W * G))) void k_attend_many(AttendArgs a) {
   constexpr int KK = D / 64, DT = D / 16, kUnits = D / 16, kPart = W > kUnits ? W / kUnits : 1, kStep = G * kPart;
   constexpr int kThreads = W * G * kWave, U = kStep * kUnits / (W * G);       // units that a wave turns
   const Walk w(a, false);
@@ -880,13 +883,18 @@ hipError_t attend_run(const AttendArgs& a, hipStream_t s) {
   const int pairs = a.n_seqs * a.hk;
   const dim3 grid((unsigned)(a.slots ? a.slots : pairs * a.tiles * a.splits));
   if constexpr (MANY) {
-    // Two groups where the rows' registers leave room for four waves a SIMD.
+    // Two groups where the rows' registers leave room for four waves a SIMD, unless
+    // there are workgroups for two to a CU (64 heads, 8 of kv, 4096 tokens 169 us
+    // and 189; 16 x 512 tokens, 32 heads 49 and 69; but whole prompts whose 512 workgroups
+    // end apart, 4096 tokens, 32 heads, 108 and 96).
     constexpr int G = D == 64 && sizeof(T) == 2 ? 2 : 1;
+    const bool two = grid.x > 2 * kSlots || (grid.x == 2 * kSlots && a.max_nb <= 32);
     if constexpr (W < kManyWaves) {
       if (a.score) k_attend_many<T, D, NB, true, W, kManyWaves / W><<<grid, kManyThreads, 0, s>>>(a);
       else k_attend_many<T, D, NB, false, W, kManyWaves / W><<<grid, kManyThreads, 0, s>>>(a);
     } else {
       if (a.score) k_attend_many<T, D, NB, true, W, 1><<<grid, kManyThreads, 0, s>>>(a);
+      else if (two) k_attend_many<T, D, NB, false, W, 1><<<grid, kManyThreads, 0, s>>>(a);
       else k_attend_many<T, D, NB, false, W, G><<<grid, G * kManyThreads, 0, s>>>(a);
     }
   } else {
@@ -952,9 +960,13 @@ AttendPlan attend_plan(int n_seqs, int hk, int group, int d, int dtype, int max_
   // and 22.3 with two; 200 of 3000, 32 and 8, D = 64 20.8 and 24.9; 200 of 8000, 64
   // and 8, D = 64 57.2 and 52.1.
   const int narrow = 16 * p.waves, most_tiles = p.many ? many_tiles(d, f32) : few_tiles(d, f32);
-  if (p.many && p.waves < kManyWaves) p.nb = most_tiles;
-  else if (p.many) p.nb = p.r_max <= narrow || shares * ((p.r_max + narrow - 1) / narrow) <= 1024 ? 1 : most_tiles;
-  else p.nb = p.r_max <= narrow ? 1 : most_tiles;
+  // Nor two for whole prompts whose workgroups would all run at once: their last rows
+  // see the most, and twice as many that begin with those end together (2048
+  // tokens, 32 heads, 8 of kv, D = 128 63 us and 72, D = 64 37 and 46).
+  auto tiles_of = [&](int nb) { return (p.r_max + narrow * nb - 1) / (narrow * nb); };
+  const bool small = shares * tiles_of(1) <= 1024 || (pairs * tiles_of(2) <= kSlots && max_q >= max_len - max_q);
+  p.nb = p.r_max <= narrow && (!p.many || p.waves == kManyWaves) ? 1 : most_tiles;
+  if (p.many && p.waves == kManyWaves && small) p.nb = 1;
   const int wg_rows = narrow * p.nb;
   p.tiles = (p.r_max + wg_rows - 1) / wg_rows;
   const int64_t wgs = pairs * p.tiles;

@@ -428,6 +428,12 @@ def test_attend_a_few_tokens_of_many_sequences(d, score, new, group):
     _few_tokens((900, 30, 880, 33, 64, 500, 1, 871, 95), f32, d, score, new, group)
 
 
+@pytest.mark.parametrize("dt,d", [(f16, 64), (f16, 128), (f32, 64)])
+def test_attend_prompts_of_many_sequences(dt, d):
+    """More workgroups than run at once; whole prompts, and one that goes on from 50 tokens."""
+    _few_tokens((350, 333, 400, 1, 350, 32, 347, 350, 350, 100, 350, 350), dt, d, False, 350, 4)
+
+
 def _few_tokens(lens, dt, d, score, new, group):
     hk = 8
     c = _filled(len(lens), hk, d, dt, lens, score=score)
