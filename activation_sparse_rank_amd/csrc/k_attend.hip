@@ -48,11 +48,11 @@ constexpr int kMaxSplits = 64;
 constexpr int kSlots = 256;                  // workgroups that run at once
 constexpr float kNoMax = -3e38f;     // reference before the first visible token
 // Weights are held times 2^6, and a lane's eight of a block may sum to 2^15
-// (the row's 32, where they are summed, to 2^16; fp16 holds 65504, what is
-// beyond sums to infinity) before the reference moves: no maximum is taken but
-// then.  What a weight loses below fp16's smallest step is at most 2^-31 of the
-// row's largest weight, so that 10^5 such tokens beside one that takes the row
-// are still counted.
+// (fp16 holds 65504) before the reference moves: no maximum is taken but then.
+// What a weight loses below fp16's smallest step is at most 2^-31 of the row's
+// largest weight, so that 10^5 such tokens beside one that takes the row are
+// still counted.  The sums are those of the unrounded weights: each weight's rounding,
+// 2^-11, is then all that the quotient is off by.
 constexpr float kBias = 6.f;
 constexpr float kMost = 0x1p15f;
 // Under this share of the wave's largest value scale a block's weights would
@@ -371,20 +371,16 @@ struct Rows {
       const f32x8 pv = {p[0], p[1], p[2], p[3], p[4], p[5], p[6], p[7]};
       pf[nb] = __builtin_convertvector(pv, f16x8);
       if constexpr (TWOP) pl[nb] = __builtin_convertvector(pv - __builtin_convertvector(pf[nb], f32x8), f16x8);
-      if constexpr (TWOP || SCORE) {
-        sum[nb] = (p[0] + p[1] + (p[2] + p[3])) + (p[4] + p[5] + (p[6] + p[7]));
-      } else {
-        // the sum of the rounded weights over the row, by a product with ones (four
-        // additions by pairs and the lanes' sum at the end: 160 us for 158, 512-token chunk)
-        const f16x8 ones = {(f16)1.f, (f16)1.f, (f16)1.f, (f16)1.f, (f16)1.f, (f16)1.f, (f16)1.f, (f16)1.f};
-        sum[nb] = mfma16(ones, pf[nb], f32x4{0.f, 0.f, 0.f, 0.f})[0];
-      }
+      sum[nb] = (p[0] + p[1] + (p[2] + p[3])) + (p[4] + p[5] + (p[6] + p[7]));
+      // Here and not behind the branch below: else the weights stay in fp32 until then
+      // (D = 128, few rows 183 registers and 145 so; 335 and 308 us for fp32 prompts).
+      asm volatile("" : "+v"(pf[nb]), "+v"(sum[nb]));
     };
     bool over = false;
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
       weights(nb);
-      over |= !(sum[nb] < (TWOP || SCORE ? kMost : 2.f * kMost));
+      over |= !(sum[nb] < kMost);
     }
     if (__any(over)) {                             // a weight passes the reference by too much: move it
 #pragma unroll
@@ -426,8 +422,7 @@ struct Rows {
 
   __device__ __forceinline__ void finish() {
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb)
-      if constexpr (TWOP || SCORE) l[nb] = row_sum(l[nb]);
+    for (int nb = 0; nb < NB; ++nb) l[nb] = row_sum(l[nb]);
     rescale(vref);
   }
 };
