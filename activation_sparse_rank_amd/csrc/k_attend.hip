@@ -51,8 +51,7 @@ constexpr float kNoMax = -3e38f;     // reference before the first visible token
 // (fp16 holds 65504) before the reference moves: no maximum is taken but then.
 // What a weight loses below fp16's smallest step is at most 2^-31 of the row's
 // largest weight, so that 10^5 such tokens beside one that takes the row are
-// still counted.  The sums are those of the unrounded weights: each weight's rounding,
-// 2^-11, is then all that the quotient is off by.
+// still counted.
 constexpr float kBias = 6.f;
 constexpr float kMost = 0x1p15f;
 // Under this share of the wave's largest value scale a block's weights would
@@ -238,12 +237,14 @@ template <typename T, int D, int NB, bool SCORE, bool TWOP>
 struct Rows {
   static constexpr int KK = D / 64, DT = D / 16;
   static constexpr bool kTwo = sizeof(T) == 4;
+  static constexpr bool kSum = TWOP || SCORE;      // sums of the unrounded weights
   int r0;
   f16x8 qf[NB][KK][2], ql[NB][kTwo ? KK : 1][2];   // lane (g, c): elements 64 kk + 16 g .. + 16 of row c
   float rs[NB];                                    // a row's power of two (fp32 rows)
   int sees[NB];
   f32x4 o[NB][DT];
-  float m[NB], l[NB];
+  float m[NB], l[NB];                              // reference; sum of the weights, a lane's share until finish()
+  float lr[NB];                                    // of the rounded weights, the row's
   float vref;                                      // o is in units of it
 
   __device__ __forceinline__ void load(const AttendArgs& a, const Walk& w, int first) {
@@ -298,7 +299,7 @@ struct Rows {
     }
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
-      m[nb] = kNoMax, l[nb] = 0.f;
+      m[nb] = kNoMax, l[nb] = lr[nb] = 0.f;
 #pragma unroll
       for (int t = 0; t < DT; ++t) o[nb][t] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
@@ -362,7 +363,7 @@ struct Rows {
     }
     const float scv = edge ? 1.f : ksc;
     f16x8 pf[NB], pl[NB];
-    float sum[NB];
+    float sum[NB], sumr[NB];
     auto weights = [&](int nb) {
       const float sc = kTwo ? (edge ? 1.f : ksc * rs[nb]) : scv, off = lrb - m[nb];
       float p[8];
@@ -371,16 +372,23 @@ struct Rows {
       const f32x8 pv = {p[0], p[1], p[2], p[3], p[4], p[5], p[6], p[7]};
       pf[nb] = __builtin_convertvector(pv, f16x8);
       if constexpr (TWOP) pl[nb] = __builtin_convertvector(pv - __builtin_convertvector(pf[nb], f32x8), f16x8);
-      sum[nb] = (p[0] + p[1] + (p[2] + p[3])) + (p[4] + p[5] + (p[6] + p[7]));
+      if constexpr (kSum) sum[nb] = (p[0] + p[1] + (p[2] + p[3])) + (p[4] + p[5] + (p[6] + p[7]));
+      if constexpr (!TWOP) {
+        // The sum of the rounded weights over the row, by a product with ones: with it
+        // the rounding of a weight that takes the row cancels.
+        const f16x8 ones = {(f16)1.f, (f16)1.f, (f16)1.f, (f16)1.f, (f16)1.f, (f16)1.f, (f16)1.f, (f16)1.f};
+        sumr[nb] = mfma16(ones, pf[nb], f32x4{0.f, 0.f, 0.f, 0.f})[0];
+      }
       // Here and not behind the branch below: else the weights stay in fp32 until then
       // (D = 128, few rows 183 registers and 145 so; 335 and 308 us for fp32 prompts).
-      asm volatile("" : "+v"(pf[nb]), "+v"(sum[nb]));
+      if constexpr (kSum) asm volatile("" : "+v"(pf[nb]), "+v"(sum[nb]));
+      else asm volatile("" : "+v"(pf[nb]));
     };
     bool over = false;
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
       weights(nb);
-      over |= !(sum[nb] < kMost);
+      over |= !(kSum ? sum[nb] < kMost : sumr[nb] < 2.f * kMost);
     }
     if (__any(over)) {                             // a weight passes the reference by too much: move it
 #pragma unroll
@@ -391,7 +399,7 @@ struct Rows {
         const float mn = fmaxf(m[nb], row_max(top));
         const float f = exp2_hw(m[nb] - mn);
         m[nb] = mn;
-        l[nb] *= f;
+        l[nb] *= f, lr[nb] *= f;
 #pragma unroll
         for (int t = 0; t < DT; ++t) o[nb][t] *= f;
         weights(nb);
@@ -399,7 +407,8 @@ struct Rows {
     }
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
-      l[nb] = __builtin_fmaf(sum[nb], ivb, l[nb]);
+      if constexpr (kSum) l[nb] = __builtin_fmaf(sum[nb], ivb, l[nb]);
+      if constexpr (!TWOP) lr[nb] = __builtin_fmaf(sumr[nb], ivb, lr[nb]);
       if constexpr (SCORE) {
         const float bw = row_sum(sum[nb]) * ivb;
         const int r = r0 + nb * 16 + c;
@@ -422,7 +431,16 @@ struct Rows {
 
   __device__ __forceinline__ void finish() {
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb) l[nb] = row_sum(l[nb]);
+    for (int nb = 0; nb < NB; ++nb) {
+      if constexpr (kSum) l[nb] = row_sum(l[nb]);
+      else l[nb] = lr[nb];
+      if constexpr (kSum && !TWOP) {
+        // rows over the rounded sum, but the sum itself unrounded (the score's blocks are)
+        const float f = lr[nb] > 0.f ? l[nb] / lr[nb] : 1.f;
+#pragma unroll
+        for (int t = 0; t < DT; ++t) o[nb][t] *= f;
+      }
+    }
     rescale(vref);
   }
 };
@@ -455,7 +473,7 @@ __global__ __launch_bounds__(kFewThreads, 2) void k_attend(AttendArgs a) {
   const int mine = start < b1 ? (b1 - start + kFewWaves - 1) / kFewWaves : 0;
 
   // The weights as two parts: the products have time while the pages come.  (As one
-  // where two tiles of D = 128 would spill: 80 us for 32 x 8 pairs of 4000 tokens, 24 rows, 46.5 so.)
+  // for two tiles of D = 128, fp16: 32 x 8 pairs of 4000 tokens, 24 rows 45.8 us and 47.5.)
   Rows<T, D, NB, SCORE, sizeof(T) == 4 || !(D == 128 && NB == 2)> rows;
   rows.load(a, w, r0);
   u32x4 rk[2 * KK], rv[DB];                         // a block's codes, as they lie in the page
@@ -576,7 +594,7 @@ __global__ __launch_bounds__(kFewThreads, 2) void k_attend(AttendArgs a) {
 // Waves to a SIMD: those of a workgroup, or two workgroups' where the registers last for them.
 template <typename T, int D, bool SCORE>
 constexpr int many_waves(int waves) { return D == 64 && sizeof(T) == 2 && !SCORE && waves == 8 ? 4 : waves / 4; }
-template <typename T, int D, int NB, bool SCORE, int W, int G>
+template <typename T, int D, int NB, bool SCORE, int W, int G, bool TWO>
 __global__ __launch_bounds__(W * G * kWave, (many_waves<T, D, SCORE>(W * G))) void k_attend_many(AttendArgs a) {
   constexpr int KK = D / 64, DT = D / 16, kUnits = D / 16, kPart = W > kUnits ? W / kUnits : 1, kStep = G * kPart;
   constexpr int kThreads = W * G * kWave, U = kStep * kUnits / (W * G);       // units that a wave turns
@@ -601,7 +619,7 @@ __global__ __launch_bounds__(W * G * kWave, (many_waves<T, D, SCORE>(W * G))) vo
   const int kmin = r0 < w.rows ? w.sees(a, r0) : 0, kmax = r0 < w.rows ? w.sees(a, r1 - 1) : 0;
 
   __shared__ u32x4 ops[2][kStep][kUnits][2][kWave];
-  Rows<T, D, NB, SCORE, sizeof(T) == 4> rows;
+  Rows<T, D, NB, SCORE, TWO || sizeof(T) == 4> rows;
   f16x8 vals[DT];                                   // a block's values, on their way while its weights are taken
   rows.load(a, w, r0);
   bool bad = false;
@@ -873,7 +891,7 @@ constexpr int few_tiles(int d, bool f32) { return d == 64 || !f32 ? 2 : 1; }
 constexpr int many_tiles(int d, bool f32) { return d == 128 && f32 ? 1 : 2; }
 
 // Launches one of the two kernels and the join.
-template <typename T, int D, int NB, bool MANY, int W = kManyWaves>
+template <typename T, int D, int NB, bool MANY, int W = kManyWaves, bool TWO = false>
 hipError_t attend_run(const AttendArgs& a, hipStream_t s) {
   const int pairs = a.n_seqs * a.hk;
   const dim3 grid((unsigned)(a.slots ? a.slots : pairs * a.tiles * a.splits));
@@ -885,12 +903,12 @@ hipError_t attend_run(const AttendArgs& a, hipStream_t s) {
     constexpr int G = D == 64 && sizeof(T) == 2 ? 2 : 1;
     const bool two = grid.x > 2 * kSlots || (grid.x == 2 * kSlots && a.max_nb <= 32);
     if constexpr (W < kManyWaves) {
-      if (a.score) k_attend_many<T, D, NB, true, W, kManyWaves / W><<<grid, kManyThreads, 0, s>>>(a);
-      else k_attend_many<T, D, NB, false, W, kManyWaves / W><<<grid, kManyThreads, 0, s>>>(a);
+      if (a.score) k_attend_many<T, D, NB, true, W, kManyWaves / W, TWO><<<grid, kManyThreads, 0, s>>>(a);
+      else k_attend_many<T, D, NB, false, W, kManyWaves / W, TWO><<<grid, kManyThreads, 0, s>>>(a);
     } else {
-      if (a.score) k_attend_many<T, D, NB, true, W, 1><<<grid, kManyThreads, 0, s>>>(a);
-      else if (two) k_attend_many<T, D, NB, false, W, 1><<<grid, kManyThreads, 0, s>>>(a);
-      else k_attend_many<T, D, NB, false, W, G><<<grid, G * kManyThreads, 0, s>>>(a);
+      if (a.score) k_attend_many<T, D, NB, true, W, 1, TWO><<<grid, kManyThreads, 0, s>>>(a);
+      else if (two) k_attend_many<T, D, NB, false, W, 1, TWO><<<grid, kManyThreads, 0, s>>>(a);
+      else k_attend_many<T, D, NB, false, W, G, TWO><<<grid, G * kManyThreads, 0, s>>>(a);
     }
   } else {
     if (a.score) k_attend<T, D, NB, true><<<grid, kFewThreads, 0, s>>>(a);
@@ -911,6 +929,8 @@ template <typename T, int D>
 hipError_t attend_nb(const AttendArgs& a, const AttendPlan& p, hipStream_t s) {
   constexpr bool f32 = sizeof(T) == 4;
   if (p.many) {
+    if constexpr (!f32)
+      if (p.two) return attend_run<T, D, 1, true, kManyWaves, true>(a, s);
     if constexpr (f32 || D == 128) {
       if (p.waves == 2) return attend_run<T, D, many_tiles(D, f32), true, 2>(a, s);
       if (p.waves == 4) return attend_run<T, D, many_tiles(D, f32), true, 4>(a, s);
@@ -947,9 +967,15 @@ AttendPlan attend_plan(int n_seqs, int hk, int group, int d, int dtype, int max_
   // same block; 72 rows 80, 107; fp32, D = 128, 24 rows 63.5, 108, D = 64, 64 rows 54.7,
   // 72.5).  Not in small calls (fp16, 8 pairs of 1500, 40 rows: 15.1 and 13.6) nor for
   // fp16 of D = 64 (72 rows: 59 and 52).
+  // The weights' second parts: over up to 512 tokens, where one weight's rounding may
+  // be the row's (error against 64 bits 2.07e-4, the output's rounding, and 2.6e-4
+  // without; 16 prompts of 512 tokens, 32 heads, D = 64 57 us and 51, 8 of D = 128 58
+  // and 43).  Longer: 3000 tokens 2.4e-4; two parts everywhere would take 287 us for 159
+  // (512 tokens over 8200, 128 heads, D = 64).
+  p.two = p.many && !f32 && p.max_nb <= 16;
   p.waves = !p.many ? 1 : kManyWaves;
   const int two = 32 * many_tiles(d, f32);             // rows of two waves
-  if (p.many && (f32 || d == 128) && shares > 256) p.waves = p.r_max <= two ? 2 : p.r_max <= 2 * two ? 4 : kManyWaves;
+  if (p.many && !p.two && (f32 || d == 128) && shares > 256) p.waves = p.r_max <= two ? 2 : p.r_max <= 2 * two ? 4 : kManyWaves;
   // Else one tile a wave while that is enough, and in small calls (counted in
   // shares of eight blocks): 100 of 1000 tokens, 32 heads, 8 of kv, D = 128 17.7 us
   // and 22.3 with two; 200 of 3000, 32 and 8, D = 64 20.8 and 24.9; 200 of 8000, 64
@@ -961,7 +987,7 @@ AttendPlan attend_plan(int n_seqs, int hk, int group, int d, int dtype, int max_
   auto tiles_of = [&](int nb) { return (p.r_max + narrow * nb - 1) / (narrow * nb); };
   const bool small = shares * tiles_of(1) <= 1024 || (pairs * tiles_of(2) <= kSlots && max_q >= max_len - max_q);
   p.nb = p.r_max <= narrow && (!p.many || p.waves == kManyWaves) ? 1 : most_tiles;
-  if (p.many && p.waves == kManyWaves && small) p.nb = 1;
+  if (p.many && p.waves == kManyWaves && (small || p.two)) p.nb = 1;
   const int wg_rows = narrow * p.nb;
   p.tiles = (p.r_max + wg_rows - 1) / wg_rows;
   const int64_t wgs = pairs * p.tiles;
