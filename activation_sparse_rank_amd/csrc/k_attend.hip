@@ -17,20 +17,22 @@
 //
 // Two ways to cut the work, by size (attend_plan).  Few rows (k_attend): the
 // pages' bytes bound the time; the eight waves of a workgroup share the rows
-// and take every eighth block.  Many rows (k_attend_many): the weights' exponentials and the
-// products do; each wave has rows of its own and all walk the blocks in
-// step, whose codes are turned to fp16 once for the workgroup, in LDS (groups of
-// waves take different blocks where the rows leave waves over).  Both
-// split the blocks over workgroups as well where the rows do not fill the
-// CUs; partial sums are joined in a fixed order (in LDS, then in k_attend_join).
+// and take every eighth block.  Many rows (k_attend_many): the weights'
+// exponentials and the products do; each wave has rows of its own and all walk
+// the blocks in step, whose codes are turned to fp16 once for the workgroup, in
+// LDS (groups of waves take different blocks where the rows leave waves over).
+// Both split the blocks over workgroups as well where the rows do not fill the
+// CUs (few rows of unlike sequences by their lengths, Shares); partial sums are
+// joined in a fixed order (in LDS, then in k_attend_join).
 //
 // Measured (streaming read 6.45 TB/s, fp16 product 1150 TFLOP/s on the same
 // card): one token of 64 heads over 131072 tokens of 8 kv heads, D = 128, 48.0 us with
 // the join (269 MB, 5.6 TB/s); 32 sequences of 16384 tokens and less with
-// scores 152 us (863 MB, 5.7 TB/s); fp32, 56 kv heads of their own, 33.9 us (180 MB, 5.3
-// TB/s); 512 tokens of 128 heads over 8200 tokens, D = 64, 158 us (133 GFLOP,
-// 844 TFLOP/s): there the instructions around the products bind, 230 k cycles
-// a SIMD beside the products' 127 k, of 350 k.
+// scores 158 us (863 MB, 5.5 TB/s); fp32, 56 kv heads of their own, 34.0 us (180
+// MB, 5.3 TB/s); 512 tokens of 128 heads over 8200 tokens, D = 64, 159 us (133
+// GFLOP, 840 TFLOP/s): there the instructions around the products bind, 230 k
+// cycles a SIMD beside the products' 143 k, of 350 k; 4096 tokens of 64 heads, 8 of
+// kv, D = 128, whole, 294 us (275 GFLOP, 935 TFLOP/s).
 #include "attn_device.h"
 
 namespace pi {
@@ -898,7 +900,7 @@ hipError_t attend_run(const AttendArgs& a, hipStream_t s) {
   if constexpr (MANY) {
     // Two groups where the rows' registers leave room for four waves a SIMD, unless
     // there are workgroups for two to a CU (64 heads, 8 of kv, 4096 tokens 169 us
-    // and 189; 16 x 512 tokens, 32 heads 49 and 69; but whole prompts whose 512 workgroups
+    // and 189; 8 x 1024 tokens, 32 heads 62 and 86; but whole prompts whose 512 workgroups
     // end apart, 4096 tokens, 32 heads, 108 and 96).
     constexpr int G = D == 64 && sizeof(T) == 2 ? 2 : 1;
     const bool two = grid.x > 2 * kSlots || (grid.x == 2 * kSlots && a.max_nb <= 32);
