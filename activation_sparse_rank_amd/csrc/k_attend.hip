@@ -65,15 +65,25 @@ __device__ __forceinline__ f32x4 mfma16(f16x8 a, f16x8 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
 }
 
-// 8 codes to fp16 values code - 128: the bytes become 1024 + code by their
-// place in the fraction of 0x6400, less 1152.  Exact.
+// 8 codes to fp16 values code - 128 (times factor, with off = -1152 factor): the
+// bytes become 1024 + code by their place in the fraction of 0x6400, less 1152.
+// Exact, with the factors of Blocks too.
+__device__ __forceinline__ f16x8 codes_f16(unsigned lo, unsigned hi, f16x2 factor, f16x2 off) {
+  const f16x2 h[4] = {as_h2(__builtin_amdgcn_perm(0x64646464u, lo, 0x04010400u)),
+                      as_h2(__builtin_amdgcn_perm(0x64646464u, lo, 0x04030402u)),
+                      as_h2(__builtin_amdgcn_perm(0x64646464u, hi, 0x04010400u)),
+                      as_h2(__builtin_amdgcn_perm(0x64646464u, hi, 0x04030402u))};
+  unsigned w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = __builtin_bit_cast(unsigned, __builtin_elementwise_fma(h[i], factor, off));
+  return __builtin_bit_cast(f16x8, u32x4{w[0], w[1], w[2], w[3]});
+}
 __device__ __forceinline__ f16x8 codes_f16(unsigned lo, unsigned hi) {
   const f16x2 off = {(f16)-1152.f, (f16)-1152.f};
-  f16x2 h[4];
-  h[0] = as_h2(__builtin_amdgcn_perm(0x64646464u, lo, 0x04010400u)) + off;
-  h[1] = as_h2(__builtin_amdgcn_perm(0x64646464u, lo, 0x04030402u)) + off;
-  h[2] = as_h2(__builtin_amdgcn_perm(0x64646464u, hi, 0x04010400u)) + off;
-  h[3] = as_h2(__builtin_amdgcn_perm(0x64646464u, hi, 0x04030402u)) + off;
+  const f16x2 h[4] = {as_h2(__builtin_amdgcn_perm(0x64646464u, lo, 0x04010400u)) + off,
+                      as_h2(__builtin_amdgcn_perm(0x64646464u, lo, 0x04030402u)) + off,
+                      as_h2(__builtin_amdgcn_perm(0x64646464u, hi, 0x04010400u)) + off,
+                      as_h2(__builtin_amdgcn_perm(0x64646464u, hi, 0x04030402u)) + off};
   return __builtin_bit_cast(f16x8, u32x4{__builtin_bit_cast(unsigned, h[0]), __builtin_bit_cast(unsigned, h[1]),
                                          __builtin_bit_cast(unsigned, h[2]), __builtin_bit_cast(unsigned, h[3])});
 }
@@ -196,7 +206,9 @@ struct Walk {
 struct Blocks {
   int page;
   float ks, lr, iv, unit;        // key scale; log2 of the weights' factor (and kBias), 1 / factor; the sums' unit
+  f16 factor;                    // of the values' codes: 0 where the value scale is 0 (the weights count all the same), else 1
   unsigned long long smalls;     // blocks whose unit is not 1
+  unsigned long long odds;       // blocks whose factor is not 1
 
   __device__ void find(const AttendArgs& a, int pair, int first, int step, int cnt, bool& bad) {
     page = 0;
@@ -230,6 +242,11 @@ struct Blocks {
     unit = ratio < kSmall ? as_f(__builtin_bit_cast(unsigned, fmaxf(ratio, kSmallest)) & 0x7f800000u) : 1.f;
     const float share = fmaxf(ratio / unit, 0x1p-60f);
     lr = log2_hw(share) + kBias, iv = 1.f / share;
+    factor = vs > 0.f ? (f16)1.f : (f16)0.f;
+    odds = __ballot(factor != (f16)1.f);
+  }
+  __device__ __forceinline__ f16 factor_of(int i) const {
+    return __builtin_bit_cast(f16, (uint16_t)__builtin_amdgcn_readlane((int)__builtin_bit_cast(uint16_t, factor), i));
   }
 };
 
@@ -325,11 +342,11 @@ struct Rows {
   }
 
   // Block b, the i-th of x.  keys(mb, kk, f) and values(t) give the operands;
-  // keys_done() is called when the last of the keys has been taken.  All the rows see
-  // the first `whole` tokens.
-  template <typename K, typename KD, typename V>
+  // keys_done() is called when the last of the keys has been taken, scale_values()
+  // before the values are where their factor is not 1.  All the rows see the first `whole` tokens.
+  template <typename K, typename KD, typename VS, typename V>
   __device__ __forceinline__ void block(const AttendArgs& a, const Walk& w, const Blocks& x, int i, int b, int whole,
-                                        K keys, KD keys_done, V values) {
+                                        K keys, KD keys_done, VS scale_values, V values) {
     const int lane = lane_id(), g = lane / 16, c = lane % 16;
     f32x4 st[NB][2];
 #pragma unroll
@@ -419,6 +436,7 @@ struct Rows {
     }
     const bool far = x.smalls >> i & 1;
     if (far) rescale(1.f / lane_f(x.unit, i));
+    if (x.odds >> i & 1) scale_values(x.factor_of(i));
 #pragma unroll
     for (int t = 0; t < DT; ++t) {
       const f16x8 v = values(t);
@@ -509,16 +527,18 @@ __global__ __launch_bounds__(kFewThreads, 2) void k_attend(AttendArgs a) {
     // condition would be waited for as if they had not been issued.)
     for (int i = 0; i < cnt; ++i) {
       const int n = i + 1 < kWave ? i + 1 : i;
+      const f16 f = x.factor_of(i);
+      const f16x2 vf = {f, f}, vo = vf * (f16)-1152.f;
       rows.block(
           a, w, x, i, start + (base + i) * kFewWaves, kmin,
           [&](int mb, int kk, int f) {
             const u32x4 v = rk[mb * KK + kk];
             return f ? codes_f16(v.z, v.w) : codes_f16(v.x, v.y);
           },
-          [&] { load_k(n); },
+          [&] { load_k(n); }, [](f16) {},            // (the factor is in codes_f16's)
           [&](int t) {
             const u32x4 v = rv[t / 2];
-            return t % 2 ? codes_f16(v.z, v.w) : codes_f16(v.x, v.y);
+            return t % 2 ? codes_f16(v.z, v.w, vf, vo) : codes_f16(v.x, v.y, vf, vo);
           });
       load_v(n);
     }
@@ -667,6 +687,10 @@ __global__ __launch_bounds__(W * G * kWave, (many_waves<T, D, SCORE>(W * G))) vo
               [&] {
 #pragma unroll
                 for (int t = 0; t < DT; ++t) vals[t] = __builtin_bit_cast(f16x8, ops[buf][j][2 * KK + t / 2][t % 2][lane]);
+              },
+              [&](f16 f) {
+#pragma unroll
+                for (int t = 0; t < DT; ++t) vals[t] *= f;
               },
               [&](int t) { return vals[t]; });
       }
