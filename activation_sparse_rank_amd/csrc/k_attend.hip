@@ -264,6 +264,7 @@ struct Rows {
   f32x4 o[NB][DT];
   float m[NB], l[NB];                              // reference; sum of the weights, a lane's share until finish()
   float lr[NB];                                    // of the rounded weights, the row's
+  float lt[NB];                                    // l of the blocks before the last fold() (fp32)
   float vref;                                      // o is in units of it
 
   __device__ __forceinline__ void load(const AttendArgs& a, const Walk& w, int first) {
@@ -318,7 +319,7 @@ struct Rows {
     }
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
-      m[nb] = kNoMax, l[nb] = lr[nb] = 0.f;
+      m[nb] = kNoMax, l[nb] = lr[nb] = lt[nb] = 0.f;
 #pragma unroll
       for (int t = 0; t < DT; ++t) o[nb][t] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
@@ -419,6 +420,7 @@ struct Rows {
         const float f = exp2_hw(m[nb] - mn);
         m[nb] = mn;
         l[nb] *= f, lr[nb] *= f;
+        if constexpr (kTwo) lt[nb] *= f;
 #pragma unroll
         for (int t = 0; t < DT; ++t) o[nb][t] *= f;
         weights(nb);
@@ -449,7 +451,21 @@ struct Rows {
     if (far) rescale(lane_f(x.unit, i));
   }
 
+  // After every 64 blocks at most: fp32 rows' sums of weights stay short chains of
+  // additions, whose roundings like terms do not add up (4096 blocks in one chain:
+  // 1e-4 of the sum; fp16 rows' outputs are rounded to more).
+  __device__ __forceinline__ void fold() {
+    if constexpr (kTwo) {
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) lt[nb] += l[nb], l[nb] = 0.f;
+    }
+  }
+
   __device__ __forceinline__ void finish() {
+    if constexpr (kTwo) {
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) l[nb] = lt[nb];
+    }
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
       if constexpr (kSum) l[nb] = row_sum(l[nb]);
@@ -542,6 +558,7 @@ __global__ __launch_bounds__(kFewThreads, 2) void k_attend(AttendArgs a) {
           });
       load_v(n);
     }
+    rows.fold();
   }
   raise_flag_if_any(a.flags, bad, PI_FLAG_KV_RANGE);
   rows.finish();
@@ -698,6 +715,7 @@ __global__ __launch_bounds__(W * G * kWave, (many_waves<T, D, SCORE>(W * G))) vo
       turn(buf);
       __syncthreads();                               // this step's operands are free, the next one's there
     }
+    rows.fold();
   }
   raise_flag_if_any(a.flags, bad, PI_FLAG_KV_RANGE);
   rows.finish();

@@ -7,8 +7,9 @@ import math
 import numpy as np
 import torch
 
+import activation_sparse_rank_amd as pi
 from helpers import host
-from test_gpu_attention import DEV, HALF, _attend, _filled
+from test_gpu_attention import DEV, HALF, Cache, _attend, _filled
 
 f16, f32 = torch.float16, torch.float32
 
@@ -107,3 +108,35 @@ class Call:
             err = np.abs(s1[:nb] - (s0[:nb] + wb.sum(0)))
             assert (err <= tol).all(), (s, h, float(np.max(err / tol)))
             assert np.array_equal(s1[nb:], s0[nb:])
+
+
+class Tail(Call):
+    """A long sequence, among so many of one token that nothing is split over workgroups (their table rows name its
+    pages too).  The first token of each of its first eight blocks takes the row; every other token's weight is 2^-bits
+    of one of theirs.  Values: the heavy tokens' are 64 of their block's scale, the others' -100 of theirs.  Keys and
+    queries have one element."""
+
+    tokens, seqs = 1 << 17, 300
+
+    def __init__(self, dt, d, new, heads, bits=21.6):
+        self.dt, self.d, self.hk, self.group, self.score = dt, d, 1, heads, False
+        nb = self.tokens // 32
+        self.c = c = Cache(1, 1, d, nb, dt)
+        c.rows = [np.zeros((2, 1, self.tokens, d), np.float16)]
+        c.pages.fill_(128)
+        at = c.table[0, 0].long()
+        c.pages[at, 1] = 28
+        c.pages[at[:8], 0, 0] = 255                              # the first token's first element: code 127
+        e = torch.arange(d, device=DEV)
+        c.pages[at[:8, None], 1, (e // 32 * 1024 + e % 16 * 16 + e // 16 % 2 * 8)[None]] = 192
+        c.scales.fill_(1.0)
+        c.scales[:, 0] = bits * math.log(2.0) / (127 * 2.0 * d ** -0.5)
+        open_ = torch.zeros((self.seqs, 1, 2, 32, d), dtype=dt, device=DEV)
+        c.c = pi.KVCache(c.pages, c.scales, open_, c.table.expand(self.seqs, 1, nb).contiguous())
+        self.lens, self.new, self.max_new = (self.tokens,) + (1,) * (self.seqs - 1), [new] + [1] * (self.seqs - 1), new
+        self.start = np.concatenate(([0], np.cumsum(self.new)))
+        self.ln = torch.tensor(self.lens, dtype=torch.int32, device=DEV)
+        self.qs = torch.from_numpy(self.start.astype(np.int32)).to(DEV)
+        self.q = torch.zeros((sum(self.new), heads, d), dtype=dt, device=DEV)
+        self.q[:, :, 0] = 2.0
+        self.at = at
