@@ -6,7 +6,8 @@
 // rows to a tile.  The block's key scale multiplies S, its value scale is an
 // addend of the exponent: p = 2^(S ks c - m + log2(vs / vref)), so neither
 // costs an instruction per element, and the sum of the weights takes
-// vs / vref out again once per block.  O^T += V^T P^T with P in fp16.  A lane holds
+// vs / vref out again once per block (far below vref, its power of two goes to the
+// codes instead, kNear).  O^T += V^T P^T with P in fp16.  A lane holds
 // the weights of 8 tokens of one row, which is what the second product's
 // operand takes from it: P never leaves the registers.  The reference
 // exponent m moves only when the weights of a block outgrow fp16's range above it (a
@@ -49,17 +50,23 @@ constexpr int kManyWaves = kManyThreads / kWave;
 constexpr int kMaxSplits = 64;
 constexpr int kSlots = 256;                  // workgroups that run at once
 constexpr float kNoMax = -3e38f;     // reference before the first visible token
-// Weights are held times 2^6, and a lane's eight of a block may sum to 2^15
+// Weights are held times 2^8, and a lane's eight of a block may sum to 2^15
 // (fp16 holds 65504) before the reference moves: no maximum is taken but then.
-// What a weight loses below fp16's smallest step is at most 2^-31 of the row's
-// largest weight, so that 10^5 such tokens beside one that takes the row are
-// still counted.
-constexpr float kBias = 6.f;
+// A block's value scale goes with its weights as far as 2^-kNear of the wave's
+// largest; farther, its power of two is the factor of the block's codes instead
+// (exact).  So what a weight loses below fp16's smallest step is at most 2^-31 of
+// the row's largest weight, in the product and in the sum of rounded weights,
+// and 10^5 such tokens beside one that takes the row are still counted.  (Less bias
+// sends more blocks the second way, more moves the reference oftener: 2^7 and 1 320
+// us, 2^8 and 2 306, 2^9 and 3 308 for 4096 tokens, 64 heads, D = 128.)
+constexpr float kBias = 8.f;
 constexpr float kMost = 0x1p15f;
-// Under this share of the wave's largest value scale a block's weights would
-// leave fp16's range: the sums are brought to the block's scale (a power of
-// two, exact, 2^-60 at least) for its product and back.
-constexpr float kSmall = 0x1p-10f, kSmallest = 0x1p-60f;
+constexpr int kNear = 2;
+// Powers of two down to 2^-14 are a normal fp16 factor of the codes.  Farther, the
+// sums are brought to the block's unit for its product and back, by up to 2^60; a
+// block whose value scale lies farther than that counts as one of scale 0, which
+// makes 0 of any code (its weights count).
+constexpr int kFactor = 14, kUnit = 60;
 
 __device__ __forceinline__ f32x4 mfma16(f16x8 a, f16x8 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
@@ -205,8 +212,8 @@ struct Walk {
 // Pages and scales of up to 64 blocks, lane i those of the i-th.
 struct Blocks {
   int page;
-  float ks, lr, iv, unit;        // key scale; log2 of the weights' factor (and kBias), 1 / factor; the sums' unit
-  f16 factor;                    // of the values' codes: 0 where the value scale is 0 (the weights count all the same), else 1
+  float ks, lr, iv, unit;        // key scale; log2 of the weights' share (and kBias), 1 / share; the sums' unit
+  f16 factor;                    // of the values' codes: value scale = share factor unit vref
   unsigned long long smalls;     // blocks whose unit is not 1
   unsigned long long odds;       // blocks whose factor is not 1
 
@@ -237,12 +244,16 @@ struct Blocks {
     return vmax;
   }
   __device__ void set_units(float vs, float vref) {
-    const float ratio = vs > 0.f ? vs / vref : 1.f;
-    smalls = __ballot(ratio < kSmall);
-    unit = ratio < kSmall ? as_f(__builtin_bit_cast(unsigned, fmaxf(ratio, kSmallest)) & 0x7f800000u) : 1.f;
-    const float share = fmaxf(ratio / unit, 0x1p-60f);
+    const bool some = vs > 0.f;
+    const int ev = __builtin_amdgcn_frexp_expf(vs), e = some ? ev - __builtin_amdgcn_frexp_expf(vref) : 0;
+    const bool near = e >= -kNear;
+    const float share = some ? __builtin_amdgcn_ldexpf(vs, near ? e - ev + 1 : 1 - ev) : 1.f;
+    const int fe = near ? 0 : (e > -kFactor ? e : -kFactor);
+    const bool none = !some || e < -kFactor - kUnit;
+    unit = near || none ? 1.f : __builtin_amdgcn_ldexpf(1.f, e - fe);
+    factor = none ? (f16)0.f : (f16)__builtin_amdgcn_ldexpf(1.f, fe);
     lr = log2_hw(share) + kBias, iv = 1.f / share;
-    factor = vs > 0.f ? (f16)1.f : (f16)0.f;
+    smalls = __ballot(unit != 1.f);
     odds = __ballot(factor != (f16)1.f);
   }
   __device__ __forceinline__ f16 factor_of(int i) const {

@@ -450,7 +450,8 @@ size_t pi_attend_workspace_bytes(const pi_kv_cache* cache, int32_t n_heads, int3
  * and all sums are fp32.  fp16: queries and codes enter the products
  * unrounded, weights as fp16 (few rows: as two fp16 parts).  fp32: queries and
  * weights enter as two fp16 parts (22 significant bits).  A weight holds to
- * half a step of its logit in fp32, as any fp32 softmax's.
+ * half a step of its logit in fp32, as any fp32 softmax's.  Value scales of a
+ * sequence's kv head may count as 0 below 2^-74 of the largest of them.
  *   q, out:    [n_tok][n_heads][head_dim]; out must not overlap q
  *   max_q:     host bound on the new rows of a sequence (1: decode)
  *   max_len:   host bound on lens, in [1, max_blocks * PI_KV_BLOCK]
