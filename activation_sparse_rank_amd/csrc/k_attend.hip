@@ -23,7 +23,7 @@
 // the blocks in step, whose codes are turned to fp16 once for the workgroup, in
 // LDS (groups of waves take different blocks where the rows leave waves over).
 // Both split the blocks over workgroups as well where the rows do not fill the
-// CUs (few rows of unlike sequences by their lengths, Shares); partial sums are
+// CUs (few rows of unlike sequences by their lengths, Shares); partial means are
 // joined in a fixed order (in LDS, then in k_attend_join).
 //
 // Measured (streaming read 6.45 TB/s, fp16 product 1150 TFLOP/s on the same
@@ -115,6 +115,9 @@ __device__ __forceinline__ float row_sum(float v) {
 __device__ __forceinline__ float row_max(float v) {
   return over_row(v, [](float a, float b) { return fmaxf(a, b); });
 }
+
+// 1 / a sum of weights; 0 where there are none.
+__device__ __forceinline__ float inverse(float sum) { return sum == 0.f ? 0.f : 1.f / sum; }
 
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
 __device__ __forceinline__ float log2_hw(float x) { return __builtin_amdgcn_logf(x); }
@@ -472,6 +475,8 @@ struct Rows {
     }
   }
 
+  // o becomes the mean of the values by their weights, l the weights' sum: a mean is
+  // no larger than the values, while a sum of them may pass fp32's range.
   __device__ __forceinline__ void finish() {
     if constexpr (kTwo) {
 #pragma unroll
@@ -481,14 +486,11 @@ struct Rows {
     for (int nb = 0; nb < NB; ++nb) {
       if constexpr (kSum) l[nb] = row_sum(l[nb]);
       else l[nb] = lr[nb];
-      if constexpr (kSum && !TWOP) {
-        // rows over the rounded sum, but the sum itself unrounded (the score's blocks are)
-        const float f = lr[nb] > 0.f ? l[nb] / lr[nb] : 1.f;
+      // (rows over the rounded sum, but the sum itself unrounded where there are scores: their blocks' are)
+      const float inv = inverse(TWOP ? l[nb] : lr[nb]);
 #pragma unroll
-        for (int t = 0; t < DT; ++t) o[nb][t] *= f;
-      }
+      for (int t = 0; t < DT; ++t) o[nb][t] = o[nb][t] * inv * vref;
     }
-    rescale(vref);
   }
 };
 
@@ -574,7 +576,7 @@ __global__ __launch_bounds__(kFewThreads, 2) void k_attend(AttendArgs a) {
   raise_flag_if_any(a.flags, bad, PI_FLAG_KV_RANGE);
   rows.finish();
 
-  // The waves' sums, added in wave order.
+  // The waves' means by their sums, added in wave order.
   __shared__ float so[kFewWaves][16][D + 4];
   __shared__ float sm[kFewWaves][16], sl[kFewWaves][16];
   __shared__ float rl[SCORE ? NB * 16 : 1];         // log2 of a row's weights, where this workgroup has all of them
@@ -592,24 +594,24 @@ __global__ __launch_bounds__(kFewThreads, 2) void k_attend(AttendArgs a) {
     float top = sm[0][row];
 #pragma unroll
     for (int y = 1; y < kFewWaves; ++y) top = fmaxf(top, sm[y][row]);
-    float sum = 0.f, v[E];
+    float sum = 0.f, f[kFewWaves], v[E];
+#pragma unroll
+    for (int y = 0; y < kFewWaves; ++y) sum += f[y] = exp2_hw(sm[y][row] - top) * sl[y][row];
+    const float inv = inverse(sum);
 #pragma unroll
     for (int k = 0; k < E; ++k) v[k] = 0.f;
 #pragma unroll
     for (int y = 0; y < kFewWaves; ++y) {
-      const float f = exp2_hw(sm[y][row] - top);
-      sum = __builtin_fmaf(f, sl[y][row], sum);
 #pragma unroll
-      for (int k = 0; k < E; ++k) v[k] = __builtin_fmaf(f, so[y][row][e0 + k], v[k]);
+      for (int k = 0; k < E; ++k) v[k] = __builtin_fmaf(f[y] * inv, so[y][row][e0 + k], v[k]);
     }
     const int64_t at = w.part_at(a, r);
     const bool whole = w.splits == 1;
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
     T* p = static_cast<T*>(a.out) + w.out_at(a, r) + e0;
 #pragma unroll
     for (int k = 0; k < E; k += 4) {
       const f32x4 y = {v[k], v[k + 1], v[k + 2], v[k + 3]};
-      if (whole) store4(p + k, y * inv);
+      if (whole) store4(p + k, y);
       else *reinterpret_cast<f32x4*>(a.part + at * D + e0 + k) = y;
     }
     if (!whole && e0 == 0) a.ml[at] = float2{top, sum};
@@ -731,7 +733,7 @@ __global__ __launch_bounds__(W * G * kWave, (many_waves<T, D, SCORE>(W * G))) vo
   raise_flag_if_any(a.flags, bad, PI_FLAG_KV_RANGE);
   rows.finish();
   if constexpr (G > 1) {
-    // The groups' sums, in the order of the groups; a lane's elements are the same in each.
+    // The groups' means by their sums, in the order of the groups; a lane's elements are the same in each.
     __shared__ float2 sml[W][NB][kWave];
     static_assert(sizeof(ops) >= sizeof(f32x4) * W * NB * DT * kWave, "a group's sums fit the operands' place");
     f32x4* so = &reinterpret_cast<f32x4*>(ops)[(wave * NB * DT) * kWave + lane];
@@ -749,9 +751,11 @@ __global__ __launch_bounds__(W * G * kWave, (many_waves<T, D, SCORE>(W * G))) vo
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
           const float2 v = sml[wave][nb][lane];
-          const float top = fmaxf(rows.m[nb], v.x), f0 = exp2_hw(rows.m[nb] - top), f1 = exp2_hw(v.x - top);
+          const float top = fmaxf(rows.m[nb], v.x);
+          const float l0 = rows.l[nb] * exp2_hw(rows.m[nb] - top), l1 = v.y * exp2_hw(v.x - top);
+          const float inv = inverse(l0 + l1), f0 = l0 * inv, f1 = l1 * inv;
           rows.m[nb] = top;
-          rows.l[nb] = rows.l[nb] * f0 + v.y * f1;
+          rows.l[nb] = l0 + l1;
 #pragma unroll
           for (int t = 0; t < DT; ++t) rows.o[nb][t] = rows.o[nb][t] * f0 + so[(nb * DT + t) * kWave] * f1;
         }
@@ -766,11 +770,10 @@ __global__ __launch_bounds__(W * G * kWave, (many_waves<T, D, SCORE>(W * G))) vo
     if (r >= w.rows) continue;
     const bool whole = a.splits == 1;
     const int64_t at = w.part_at(a, r);
-    const float inv = rows.l[nb] == 0.f ? 0.f : 1.f / rows.l[nb];
     T* p = static_cast<T*>(a.out) + w.out_at(a, r) + 4 * g;
 #pragma unroll
     for (int t = 0; t < DT; ++t) {
-      if (whole) store4(p + 16 * t, rows.o[nb][t] * inv);
+      if (whole) store4(p + 16 * t, rows.o[nb][t]);
       else *reinterpret_cast<f32x4*>(a.part + at * D + 16 * t + 4 * g) = rows.o[nb][t];
     }
     if ((!whole || SCORE) && g == 0) a.ml[at] = float2{rows.m[nb], rows.l[nb]};
@@ -789,7 +792,7 @@ __device__ __forceinline__ float2 row_ml(const AttendArgs& a, int pairs, int pai
   return v;
 }
 
-// Joins the splits' sums into rows (workgroups below row_groups: kFewSplits
+// Joins the splits' means into rows (workgroups below row_groups: kFewSplits
 // splits or less, a thread adds them and a workgroup takes as many rows as it
 // has threads for; more, a workgroup takes one row and shares the splits), and
 // adds the blocks' weights to the score (the others, kAtThreads / score_lanes()
@@ -835,18 +838,19 @@ __global__ __launch_bounds__(kAtThreads) void k_attend_join(AttendArgs a, int ro
         float to = top;
 #pragma unroll
         for (int k = 0; k < kFewSplits; ++k) to = i + k < n ? fmaxf(to, v[k].x) : to;
-        const float down = exp2_hw(top - to);
-        top = to, sum *= down, o *= down;
+        const float before = sum * exp2_hw(top - to);
+        float f[kFewSplits];
+        top = to, sum = before;
 #pragma unroll
-        for (int k = 0; k < kFewSplits; ++k) {
-          const float f = i + k < n ? exp2_hw(v[k].x - top) : 0.f;
-          sum = i + k < n ? __builtin_fmaf(f, v[k].y, sum) : sum;
-          o += i + k < n ? f * x[k] : f32x4{0.f, 0.f, 0.f, 0.f};
-        }
+        for (int k = 0; k < kFewSplits; ++k) sum += f[k] = i + k < n ? exp2_hw(v[k].x - top) * v[k].y : 0.f;
+        const float inv = inverse(sum);
+        o *= before * inv;
+#pragma unroll
+        for (int k = 0; k < kFewSplits; ++k) o += i + k < n ? f[k] * inv * x[k] : f32x4{0.f, 0.f, 0.f, 0.f};
       }
       const int h = pair % a.hk;
       T* p = static_cast<T*>(a.out) + (int64_t)(q.q0 + r / a.group) * a.o_ts + (int64_t)(h * a.group + r % a.group) * a.o_hs;
-      store4(p + e, o * (sum == 0.f ? 0.f : 1.f / sum));
+      store4(p + e, o);
       return;
     }
     __shared__ f32x4 acc[G][L];
@@ -869,8 +873,8 @@ __global__ __launch_bounds__(kAtThreads) void k_attend_join(AttendArgs a, int ro
     float top = v.x;
 #pragma unroll
     for (int y = 32; y >= 1; y >>= 1) top = fmaxf(top, __shfl_xor(top, y, kWave));
-    const float f = exp2_hw(v.x - top);
-    const float sum = wave_sum(f * v.y);
+    float f = exp2_hw(v.x - top) * v.y;
+    f *= inverse(wave_sum(f));
     f32x4 o = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int k = 0; k < N; ++k) {
@@ -883,7 +887,6 @@ __global__ __launch_bounds__(kAtThreads) void k_attend_join(AttendArgs a, int ro
     if (part) return;
 #pragma unroll
     for (int i = 1; i < G; ++i) o += acc[i][e / 4];
-    o *= sum == 0.f ? 0.f : 1.f / sum;
     const int h = pair % a.hk;
     T* p = static_cast<T*>(a.out) + (int64_t)(q.q0 + r / a.group) * a.o_ts + (int64_t)(h * a.group + r % a.group) * a.o_hs + e;
     store4(p, o);

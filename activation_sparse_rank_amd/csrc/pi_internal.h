@@ -307,7 +307,7 @@ struct AttendArgs {
   int n_seqs, hk, group, n_tok, max_q, max_len, max_blocks, n_pages;
   float scale;              // of the logits, times log2(e)
   int r_max, max_nb, tiles, splits, slots, splits_max;
-  float* part;              // [splits_max][n_seqs * hk][r_max][d] sums of a split's weights times values
+  float* part;              // [splits_max][n_seqs * hk][r_max][d] means of a split's values by their weights
   float share_even, share_safe;
   float2* ml;               // [splits_max][n_seqs * hk][r_max] reference exponent and sum of the weights
   float* lse;               // [n_seqs * hk][max_nb][r_max] log2 of a block's weights
