@@ -62,6 +62,13 @@ constexpr float kNoMax = -3e38f;     // reference before the first visible token
 constexpr float kBias = 8.f;
 constexpr float kMost = 0x1p15f;
 constexpr int kNear = 2;
+// k_attend_many has fp16 rows' weights as one fp16 part, which leaves half a step of
+// fp16 of each weight in the output, unless the rows see 512 tokens or less (where one
+// weight's rounding may be the row's: error against 64 bits 2.07e-4, the output's own
+// rounding, and 2.6e-4 with one part; 3000 tokens 2.4e-4 with one) or a kv head has 32 rows
+// or less, as k_attend's; by what the rows see and are, not by the call's bounds.  Two
+// parts everywhere would take 287 us for 159 (512 tokens over 8200, 128 heads, D = 64).
+constexpr int kTwoTokens = 512, kTwoRows = 32;
 // Powers of two down to 2^-14 are a normal fp16 factor of the codes.  Farther, the
 // sums are brought to the block's unit for its product and back, by up to 2^60; a
 // block whose value scale lies farther than that counts as one of scale 0, which
@@ -521,9 +528,9 @@ __global__ __launch_bounds__(kFewThreads, 2) void k_attend(AttendArgs a) {
   const int start = b0 + wave;
   const int mine = start < b1 ? (b1 - start + kFewWaves - 1) / kFewWaves : 0;
 
-  // The weights as two parts: the products have time while the pages come.  (As one
-  // for two tiles of D = 128, fp16: 32 x 8 pairs of 4000 tokens, 24 rows 45.8 us and 47.5.)
-  Rows<T, D, NB, SCORE, sizeof(T) == 4 || !(D == 128 && NB == 2)> rows;
+  // The weights as two parts: the products have time while the pages come (D = 128,
+  // fp16, 32 x 8 pairs of 4000 tokens, 24 rows 48.2 us for 46.4 with one).
+  Rows<T, D, NB, SCORE, true> rows;
   rows.load(a, w, r0);
   u32x4 rk[2 * KK], rv[DB];                         // a block's codes, as they lie in the page
   bool bad = false;
@@ -646,22 +653,21 @@ __global__ __launch_bounds__(kFewThreads, 2) void k_attend(AttendArgs a) {
 // Waves to a SIMD: those of a workgroup, or two workgroups' where the registers last for them.
 template <typename T, int D, bool SCORE>
 constexpr int many_waves(int waves) { return D == 64 && sizeof(T) == 2 && !SCORE && waves == 8 ? 4 : waves / 4; }
-template <typename T, int D, int NB, bool SCORE, int W, int G, bool TWO>
-__global__ __launch_bounds__(W * G * kWave, (many_waves<T, D, SCORE>(W * G))) void k_attend_many(AttendArgs a) {
-  constexpr int KK = D / 64, DT = D / 16, kUnits = D / 16, kPart = W > kUnits ? W / kUnits : 1, kStep = G * kPart;
-  constexpr int kThreads = W * G * kWave, U = kStep * kUnits / (W * G);       // units that a wave turns
-  const Walk w(a, false);
+template <int D, int NB, int W, int G>
+struct ManyLds {
+  static constexpr int kUnits = D / 16, kPart = W > kUnits ? W / kUnits : 1, kStep = G * kPart;
+  u32x4 ops[2][kStep][kUnits][2][kWave];
+  float2 sml[G > 1 ? W : 1][NB][kWave];
+};
+
+// The rows from g0 on, as many as the workgroup's waves hold; the weights as two parts (TWO) or one.
+template <typename T, int D, int NB, bool SCORE, int W, int G, bool TWO, typename L>
+__device__ __forceinline__ void many_rows(const AttendArgs& a, const Walk& w, L& lds, int g0) {
+  constexpr int KK = D / 64, DT = D / 16, kUnits = L::kUnits, kPart = L::kPart, kStep = L::kStep;
+  constexpr int U = kStep * kUnits / (W * G);       // units that a wave turns
+  constexpr int kRows = 16 * NB * W;
   const int lane = lane_id(), g = lane / 16, c = lane % 16;
   const int wave = wave_id() % W, group = wave_id() / W;
-  if (!w.q.ok) {
-    if (w.split == 0) nan_rows<T>(a, w.q, w.h, D, (int64_t)w.tile * kThreads + threadIdx.x, (int64_t)a.tiles * kThreads);
-    if (threadIdx.x == 0) raise_flag(a.flags, PI_FLAG_KV_RANGE);
-    return;
-  }
-  constexpr int kRows = 16 * NB * W;
-  // The last rows see the most: they begin first.
-  const int g0 = (a.tiles - 1 - w.tile) * kRows;
-  if (g0 >= w.rows) return;
   const int g1 = g0 + kRows < w.rows ? g0 + kRows : w.rows;
   const int nbk = (w.sees(a, g1 - 1) + kBlk - 1) / kBlk;
   const int per = (nbk + a.splits - 1) / a.splits;
@@ -670,8 +676,7 @@ __global__ __launch_bounds__(W * G * kWave, (many_waves<T, D, SCORE>(W * G))) vo
   const int r1 = r0 + 16 * NB < w.rows ? r0 + 16 * NB : w.rows;
   const int kmin = r0 < w.rows ? w.sees(a, r0) : 0, kmax = r0 < w.rows ? w.sees(a, r1 - 1) : 0;
 
-  __shared__ u32x4 ops[2][kStep][kUnits][2][kWave];
-  Rows<T, D, NB, SCORE, TWO || sizeof(T) == 4> rows;
+  Rows<T, D, NB, SCORE, TWO> rows;
   f16x8 vals[DT];                                   // a block's values, on their way while its weights are taken
   rows.load(a, w, r0);
   bool bad = false;
@@ -693,8 +698,8 @@ __global__ __launch_bounds__(W * G * kWave, (many_waves<T, D, SCORE>(W * G))) vo
       for (int k = 0; k < U; ++k) {
         const int u = wave_id() * U + k;
         const u32x4 v = next[k];
-        ops[buf][u / kUnits][u % kUnits][0][lane] = __builtin_bit_cast(u32x4, codes_f16(v.x, v.y));
-        ops[buf][u / kUnits][u % kUnits][1][lane] = __builtin_bit_cast(u32x4, codes_f16(v.z, v.w));
+        lds.ops[buf][u / kUnits][u % kUnits][0][lane] = __builtin_bit_cast(u32x4, codes_f16(v.x, v.y));
+        lds.ops[buf][u / kUnits][u % kUnits][1][lane] = __builtin_bit_cast(u32x4, codes_f16(v.z, v.w));
       }
     };
     fetch(0);
@@ -713,10 +718,10 @@ __global__ __launch_bounds__(W * G * kWave, (many_waves<T, D, SCORE>(W * G))) vo
         if (i + j < cnt && b * kBlk < kmax)
           rows.block(
               a, w, x, i + j, b, kmin,
-              [&](int mb, int kk, int f) { return __builtin_bit_cast(f16x8, ops[buf][j][mb * KK + kk][f][lane]); },
+              [&](int mb, int kk, int f) { return __builtin_bit_cast(f16x8, lds.ops[buf][j][mb * KK + kk][f][lane]); },
               [&] {
 #pragma unroll
-                for (int t = 0; t < DT; ++t) vals[t] = __builtin_bit_cast(f16x8, ops[buf][j][2 * KK + t / 2][t % 2][lane]);
+                for (int t = 0; t < DT; ++t) vals[t] = __builtin_bit_cast(f16x8, lds.ops[buf][j][2 * KK + t / 2][t % 2][lane]);
               },
               [&](f16 f) {
 #pragma unroll
@@ -734,14 +739,13 @@ __global__ __launch_bounds__(W * G * kWave, (many_waves<T, D, SCORE>(W * G))) vo
   rows.finish();
   if constexpr (G > 1) {
     // The groups' means by their sums, in the order of the groups; a lane's elements are the same in each.
-    __shared__ float2 sml[W][NB][kWave];
-    static_assert(sizeof(ops) >= sizeof(f32x4) * W * NB * DT * kWave, "a group's sums fit the operands' place");
-    f32x4* so = &reinterpret_cast<f32x4*>(ops)[(wave * NB * DT) * kWave + lane];
+    static_assert(sizeof(lds.ops) >= sizeof(f32x4) * W * NB * DT * kWave, "a group's means fit the operands' place");
+    f32x4* so = &reinterpret_cast<f32x4*>(lds.ops)[(wave * NB * DT) * kWave + lane];
     for (int y = 1; y < G; ++y) {
       if (group == y) {
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
-          sml[wave][nb][lane] = float2{rows.m[nb], rows.l[nb]};
+          lds.sml[wave][nb][lane] = float2{rows.m[nb], rows.l[nb]};
 #pragma unroll
           for (int t = 0; t < DT; ++t) so[(nb * DT + t) * kWave] = rows.o[nb][t];
         }
@@ -750,7 +754,7 @@ __global__ __launch_bounds__(W * G * kWave, (many_waves<T, D, SCORE>(W * G))) vo
       if (group == 0) {
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
-          const float2 v = sml[wave][nb][lane];
+          const float2 v = lds.sml[wave][nb][lane];
           const float top = fmaxf(rows.m[nb], v.x);
           const float l0 = rows.l[nb] * exp2_hw(rows.m[nb] - top), l1 = v.y * exp2_hw(v.x - top);
           const float inv = inverse(l0 + l1), f0 = l0 * inv, f1 = l1 * inv;
@@ -777,6 +781,36 @@ __global__ __launch_bounds__(W * G * kWave, (many_waves<T, D, SCORE>(W * G))) vo
       else *reinterpret_cast<f32x4*>(a.part + at * D + 16 * t + 4 * g) = rows.o[nb][t];
     }
     if ((!whole || SCORE) && g == 0) a.ml[at] = float2{rows.m[nb], rows.l[nb]};
+  }
+}
+
+template <typename T, int D, int NB, bool SCORE, int W, int G, bool TWO>
+__global__ __launch_bounds__(W * G * kWave, (many_waves<T, D, SCORE>(W * G))) void k_attend_many(AttendArgs a) {
+  constexpr int kThreads = W * G * kWave, kRows = 16 * NB * W;
+  const Walk w(a, false);
+  if (!w.q.ok) {
+    if (w.split == 0) nan_rows<T>(a, w.q, w.h, D, (int64_t)w.tile * kThreads + threadIdx.x, (int64_t)a.tiles * kThreads);
+    if (threadIdx.x == 0) raise_flag(a.flags, PI_FLAG_KV_RANGE);
+    return;
+  }
+  // The last rows see the most: they begin first.
+  const int g0 = (a.tiles - 1 - w.tile) * kRows;
+  if (g0 >= w.rows) return;
+  __shared__ ManyLds<D, NB, W, G> lds;
+  if constexpr (TWO || sizeof(T) == 4) {
+    many_rows<T, D, NB, SCORE, W, G, true>(a, w, lds, g0);
+  } else if (w.sees(a, g0) <= kTwoTokens || w.rows <= kTwoRows) {
+    // D = 64: a tile of each wave at a time, as two tiles' registers would be spilled in
+    // the other branch too (512 tokens over 8200, 128 heads 207 us for 162).  D = 128: at
+    // once (4096 tokens, 64 heads 311 us for 319).
+    constexpr int B = D == 64 ? 1 : NB;
+#pragma unroll 1
+    for (int at = g0; at < g0 + kRows && at < w.rows; at += 16 * B * W) {
+      if (at > g0) __syncthreads();
+      many_rows<T, D, B, SCORE, W, G, true>(a, w, lds, at);
+    }
+  } else {
+    many_rows<T, D, NB, SCORE, W, G, false>(a, w, lds, g0);
   }
 }
 
@@ -1025,12 +1059,9 @@ AttendPlan attend_plan(int n_seqs, int hk, int group, int d, int dtype, int max_
   // same block; 72 rows 80, 107; fp32, D = 128, 24 rows 63.5, 108, D = 64, 64 rows 54.7,
   // 72.5).  Not in small calls (fp16, 8 pairs of 1500, 40 rows: 15.1 and 13.6) nor for
   // fp16 of D = 64 (72 rows: 59 and 52).
-  // The weights' second parts: over up to 512 tokens, where one weight's rounding may
-  // be the row's (error against 64 bits 2.07e-4, the output's rounding, and 2.6e-4
-  // without; 16 prompts of 512 tokens, 32 heads, D = 64 57 us and 51, 8 of D = 128 58
-  // and 43).  Longer: 3000 tokens 2.4e-4; two parts everywhere would take 287 us for 159
-  // (512 tokens over 8200, 128 heads, D = 64).
-  p.two = p.many && !f32 && p.max_nb <= 16;
+  // All rows see kTwoTokens at most: no other kernel is needed, and one tile a wave (16
+  // prompts of 512 tokens, 32 heads, D = 64 57 us, with one part 51; 8 of D = 128 58 and 43).
+  p.two = p.many && !f32 && p.max_nb * kBlk <= kTwoTokens;
   p.waves = !p.many ? 1 : kManyWaves;
   const int two = 32 * many_tiles(d, f32);             // rows of two waves
   if (p.many && !p.two && (f32 || d == 128) && shares > 256) p.waves = p.r_max <= two ? 2 : p.r_max <= 2 * two ? 4 : kManyWaves;

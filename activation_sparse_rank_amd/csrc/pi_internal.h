@@ -279,7 +279,7 @@ hipError_t launch_kv_read(const CacheArgs& a, hipStream_t s);
 struct AttendPlan {
   int nb;                   // 16-row tiles per wave
   bool many;                // each wave has rows of its own; else the waves of a workgroup share rows and split the blocks
-  bool two;                 // many: fp16 rows' weights as two parts
+  bool two;                 // many: all fp16 rows' weights as two parts (else by what they see)
   int waves;                // that have rows of their own, in a workgroup (many; the others take other blocks)
   int tiles;                // workgroups over the rows of a (sequence, kv head)
   int splits;               // workgroups over the blocks (with slots: on average)

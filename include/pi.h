@@ -447,9 +447,11 @@ size_t pi_attend_workspace_bytes(const pi_kv_cache* cache, int32_t n_heads, int3
  * that a row sees, for query head j with kv head j / (n_heads / n_kv_heads).
  * Row i of a sequence's new rows sees tokens 0 .. lens - new + i (itself the
  * last); a row that sees none gives zeros.  Logits, the softmax's statistics
- * and all sums are fp32.  fp16: queries and codes enter the products
- * unrounded, weights as fp16 (few rows: as two fp16 parts).  fp32: queries and
- * weights enter as two fp16 parts (22 significant bits).  A weight holds to
+ * and all sums are fp32.  Queries and codes enter the products unrounded (fp32
+ * queries as two fp16 parts, 22 significant bits).  Weights enter as two fp16 parts,
+ * too, except those of fp16 rows that see more than 512 tokens in a sequence with more than 32
+ * rows to a kv head (new tokens times n_heads / n_kv_heads): they may enter as one, 11
+ * bits, over the sum of the rounded weights.  A weight holds to
  * half a step of its logit in fp32, as any fp32 softmax's.  Value scales of a
  * sequence's kv head may count as 0 below 2^-74 of the largest of them.
  *   q, out:    [n_tok][n_heads][head_dim]; out must not overlap q
