@@ -143,8 +143,8 @@ def kv_append(cache: KVCache, k, v, lens, q_start=None, max_new=None, stream=Non
     """Append token rows to the cache (pi_kv_append).  ``lens`` (int32
     [n_seqs]) counts the tokens held after the call; ``q_start`` (int32
     [n_seqs + 1]) gives each sequence's rows, at most ``max_new`` of them
-    (default: all rows of k); without it every sequence has max_new rows, one after the other
-    (default: n_tok / n_seqs)."""
+    (default: all rows of k, or as many as a table row holds); without it every
+    sequence has max_new rows, one after the other (default: n_tok / n_seqs)."""
     st = (_native or load_native()).kv_append(cache._addr, cache._dev, k, v, lens, q_start, max_new, _handle(stream))
     if st:
         raise PiError(st, "pi_kv_append")
@@ -183,7 +183,7 @@ def attend(cache: KVCache, q, lens, out, q_start=None, max_q=None, max_len=None,
 
     ``q``, ``out``: [n_tok, n_heads, head_dim]; the rows of a sequence are its
     last tokens, each sees the tokens up to itself.  ``lens``, ``q_start``,
-    ``max_q`` as for kv_append; ``max_len``: bound on lens (default: what the
+    ``max_q`` as for kv_append (max_q by default all rows of q); ``max_len``: bound on lens (default: what the
     table holds); ``scale``: 1 / sqrt(head_dim) by default; ``add_score``: add the
     weights of each block to cache.score.  ``ws`` from alloc_attend_workspace
     with the same bounds (one is allocated where it is None)."""

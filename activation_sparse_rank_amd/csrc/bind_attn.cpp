@@ -11,6 +11,7 @@
 
 #include <c10/core/DeviceGuard.h>
 #include <c10/hip/HIPStream.h>
+#include <algorithm>
 #include <dlfcn.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -125,7 +126,8 @@ struct Bounds {
   const int32_t *lens, *q_start;
   int max_q;
 };
-Bounds bounds(const pi_kv_cache* c, PyObject* lens, PyObject* q_start, PyObject* max_q, int n_tok, int dev) {
+// `most`: what the bound is at most where it is left out beside q_start.
+Bounds bounds(const pi_kv_cache* c, PyObject* lens, PyObject* q_start, PyObject* max_q, int n_tok, int dev, int64_t most) {
   Bounds b;
   b.lens = int32s(lens, "lens", c->n_seqs, dev);
   b.q_start = nullptr;
@@ -136,7 +138,7 @@ Bounds bounds(const pi_kv_cache* c, PyObject* lens, PyObject* q_start, PyObject*
     b.max_q = (int)m;
   } else {
     b.q_start = int32s(q_start, "q_start", (int64_t)c->n_seqs + 1, dev);
-    b.max_q = max_q == Py_None ? n_tok : (int)integer(max_q, "the bound on a sequence's rows");
+    b.max_q = max_q == Py_None ? (int)std::min<int64_t>(n_tok, most) : (int)integer(max_q, "the bound on a sequence's rows");
   }
   return b;
 }
@@ -171,7 +173,8 @@ int64_t kv_rows(PyObject* const* a, Py_ssize_t n) {
   const Rows k = rows(a[2], READ ? "k_out" : "k", c->n_kv_heads, c->head_dim, dt, dev);
   const Rows v = rows(a[3], READ ? "v_out" : "v", c->n_kv_heads, c->head_dim, dt, dev);
   same_tokens(k, v, READ ? "k_out and v_out" : "k and v");
-  const Bounds b = bounds(c, a[4], a[5], a[6], k.n_tok, dev);
+  // (a sequence's new rows are among those that its table row holds)
+  const Bounds b = bounds(c, a[4], a[5], a[6], k.n_tok, dev, (int64_t)c->max_blocks * PI_KV_BLOCK);
   if (k.n_tok == 0) return PI_OK;
   void* s = stream_of(a[7], dev);
   return queue(dev, [&] {
@@ -188,7 +191,7 @@ int64_t attend(PyObject* const* a, Py_ssize_t n) {
   const at::ScalarType dt = scalar_of(c->dtype);
   const Rows q = rows(a[2], "q", -1, c->head_dim, dt, dev), out = rows(a[4], "out", q.heads, c->head_dim, dt, dev);
   same_tokens(q, out, "q and out");
-  const Bounds b = bounds(c, a[3], a[5], a[6], q.n_tok, dev);
+  const Bounds b = bounds(c, a[3], a[5], a[6], q.n_tok, dev, q.n_tok);
   const int max_len = (int)integer(a[7], "max_len"), add_score = PyObject_IsTrue(a[9]);
   const float scale = (float)real(a[8]);
   const at::Tensor& ws = tensor(a[10], "ws");
