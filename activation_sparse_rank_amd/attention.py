@@ -115,14 +115,20 @@ class KVCache:
         if open.dim() != 5 or open.shape[2] != 2 or open.shape[3] != L.PI_KV_BLOCK or open.dtype not in _DTYPES:
             raise ValueError("open must be float16 or float32 [n_seqs, n_kv_heads, 2, 32, head_dim]")
         s, h, _, _, d = open.shape
+        if s < 1 or h < 1:
+            raise ValueError("open must have sequences and heads")
         if d not in (64, 128):
             raise ValueError("head_dim must be 64 or 128")
         if pages.dtype != torch.uint8 or pages.dim() != 3 or pages.shape[1:] != (2, L.PI_KV_BLOCK * d):
             raise ValueError("pages must be uint8 [n_pages, 2, 32 * head_dim]")
+        if pages.shape[0] < 1:
+            raise ValueError("pages must have a page")
         if scales.dtype != torch.float32 or scales.shape != (pages.shape[0], 2):
             raise ValueError("scales must be float32 [n_pages, 2]")
         if table.dtype != torch.int32 or table.dim() != 3 or table.shape[:2] != (s, h):
             raise ValueError("table must be int32 [n_seqs, n_kv_heads, max_blocks]")
+        if table.shape[2] < 1:
+            raise ValueError("table must have blocks")
         if score is not None:
             _dev(score, "score")
             if score.dtype != torch.float32 or score.shape != table.shape:

@@ -95,6 +95,12 @@ const D* descriptor(PyObject* o) {
   return static_cast<const D*>(p);
 }
 
+const pi_kv_cache* cache_of(PyObject* o) {
+  const auto* c = descriptor<pi_kv_cache>(o);
+  if (c->n_seqs < 1) fail(PyExc_ValueError, "%s must have sequences", "the cache");      // (rows are divided by them)
+  return c;
+}
+
 // None: the device's current stream; else a handle.
 void* stream_of(PyObject* o, int dev) {
   if (o == Py_None) return c10::hip::getCurrentHIPStream((c10::DeviceIndex)dev).stream();
@@ -167,7 +173,7 @@ int64_t qk_rope(PyObject* const* a, Py_ssize_t n) {
 template <bool READ>
 int64_t kv_rows(PyObject* const* a, Py_ssize_t n) {
   arguments(n, 8);
-  const pi_kv_cache* c = descriptor<pi_kv_cache>(a[0]);
+  const pi_kv_cache* c = cache_of(a[0]);
   const int dev = (int)integer(a[1], "dev");
   const at::ScalarType dt = scalar_of(c->dtype);
   const Rows k = rows(a[2], READ ? "k_out" : "k", c->n_kv_heads, c->head_dim, dt, dev);
@@ -186,7 +192,7 @@ int64_t kv_rows(PyObject* const* a, Py_ssize_t n) {
 // (cache, dev, q, lens, out, q_start, max_q, max_len, scale, add_score, ws, stream)
 int64_t attend(PyObject* const* a, Py_ssize_t n) {
   arguments(n, 12);
-  const pi_kv_cache* c = descriptor<pi_kv_cache>(a[0]);
+  const pi_kv_cache* c = cache_of(a[0]);
   const int dev = (int)integer(a[1], "dev");
   const at::ScalarType dt = scalar_of(c->dtype);
   const Rows q = rows(a[2], "q", -1, c->head_dim, dt, dev), out = rows(a[4], "out", q.heads, c->head_dim, dt, dev);

@@ -1,4 +1,4 @@
-"""Bounds that a caller leaves out."""
+"""Bounds that a caller leaves out, and sizes of 0."""
 
 import numpy as np
 import pytest
@@ -35,3 +35,11 @@ def test_append_and_read_without_a_bound():
     want = [torch.zeros_like(x) for x in out]
     pi.kv_read(c.c, lens, want[0], want[1], q_start=qs, max_new=128)
     assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1])
+
+
+@pytest.mark.parametrize("seqs,heads,blocks,pages", [(0, 2, 4, 8), (2, 0, 4, 8), (2, 2, 0, 8), (2, 2, 4, 0)])
+def test_caches_without_sequences_heads_blocks_or_pages(seqs, heads, blocks, pages):
+    with pytest.raises(ValueError, match="must have"):
+        pi.KVCache(torch.zeros((pages, 2, 2048), dtype=torch.uint8, device=DEV), torch.zeros((pages, 2), device=DEV),
+                   torch.zeros((seqs, heads, 2, 32, 64), dtype=torch.float16, device=DEV),
+                   torch.zeros((seqs, heads, blocks), dtype=torch.int32, device=DEV))
