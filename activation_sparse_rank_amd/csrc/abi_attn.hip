@@ -73,8 +73,6 @@ pi_status cache_args(const pi_kv_cache* c, const int32_t* lens, const int32_t* q
   if ((st = check_rows(k, k_ts, k_hs, c->n_kv_heads, n_tok, c->head_dim, c->dtype)) != PI_OK) return st;
   if ((st = check_rows(v, v_ts, v_hs, c->n_kv_heads, n_tok, c->head_dim, c->dtype)) != PI_OK) return st;
   if (!al4(lens) || !al4(q_start)) return PI_E_ALIGN;
-  const int64_t count = ((int64_t)max_new + 2 * PI_KV_BLOCK - 2) / PI_KV_BLOCK;
-  if ((int64_t)c->n_seqs * c->n_kv_heads * 2 * count > kMaxInt) return PI_E_SHAPE;
   a->n_seqs = c->n_seqs;
   a->hk = c->n_kv_heads;
   a->d = c->head_dim;
@@ -91,7 +89,7 @@ pi_status cache_args(const pi_kv_cache* c, const int32_t* lens, const int32_t* q
   a->n_tok = n_tok;
   a->kv[0] = head_rows(k, k_ts, k_hs, c->n_kv_heads);
   a->kv[1] = head_rows(v, v_ts, v_hs, c->n_kv_heads);
-  return PI_OK;
+  return pi::kv_cache_threads(*a) > pi::kMaxThreads ? PI_E_SHAPE : PI_OK;
 }
 
 pi_status plan_for(const pi_kv_cache* c, int n_heads, int max_q, int max_len, bool score, pi::AttendPlan* p) {
@@ -103,7 +101,7 @@ pi_status plan_for(const pi_kv_cache* c, int n_heads, int max_q, int max_len, bo
   if ((int64_t)c->n_seqs * n_heads * max_q > kMaxInt / 2) return PI_E_SHAPE;
   *p = pi::attend_plan(c->n_seqs, c->n_kv_heads, group, c->head_dim, c->dtype, max_q, max_len, score);
   const int64_t pairs = (int64_t)c->n_seqs * c->n_kv_heads;
-  if (pairs * p->tiles * p->splits > kMaxInt || pairs * (p->r_max + p->max_nb) > kMaxInt) return PI_E_SHAPE;
+  if (p->threads > pi::kMaxThreads || pairs * (p->r_max + p->max_nb) > kMaxInt) return PI_E_SHAPE;
   return PI_OK;
 }
 
@@ -172,6 +170,7 @@ pi_status pi_qk_rope(const pi_rope* rope, const void* q, int64_t q_tok_stride, i
   a.w[0] = rope->q_norm;
   a.w[1] = rope->k_norm;
   a.pos = pos;
+  if (pi::qk_rope_threads(a) > pi::kMaxThreads) return PI_E_SHAPE;
   const hipError_t e = pi::launch_qk_rope(a, static_cast<hipStream_t>(stream));
   return e == hipSuccess ? PI_OK : pi::hip_failed(e);
 }
@@ -297,6 +296,7 @@ pi_status pi_kv_evict(const int32_t* table, const float* score, const int32_t* l
   a.table_out = table_out;
   a.score_out = score_out;
   a.lens_out = lens_out;
+  if (pi::kv_evict_threads(a) > pi::kMaxThreads) return PI_E_SHAPE;
   const hipError_t e = pi::launch_kv_evict(a, static_cast<hipStream_t>(stream));
   return e == hipSuccess ? PI_OK : pi::hip_failed(e);
 }

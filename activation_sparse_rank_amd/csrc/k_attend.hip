@@ -46,6 +46,7 @@ typedef float f32x8 __attribute__((ext_vector_type(8)));
 constexpr int kAtThreads = 256;              // k_attend_join
 constexpr int kFewThreads = 512, kFewWaves = kFewThreads / kWave;
 constexpr int kManyThreads = 512;
+static_assert(kManyThreads == kFewThreads, "attend_plan counts the threads of either");
 constexpr int kManyWaves = kManyThreads / kWave;
 constexpr int kMaxSplits = 64;
 constexpr int kSlots = 256;                  // workgroups that run at once
@@ -984,7 +985,7 @@ constexpr int many_tiles(int d, bool f32) { return d == 128 && f32 ? 1 : 2; }
 
 // Launches one of the two kernels and the join.
 template <typename T, int D, int NB, bool MANY, int W = kManyWaves, bool TWO = false>
-hipError_t attend_run(const AttendArgs& a, hipStream_t s) {
+hipError_t attend_run(const AttendArgs& a, const AttendPlan& p, hipStream_t s) {
   const int pairs = a.n_seqs * a.hk;
   const dim3 grid((unsigned)(a.slots ? a.slots : pairs * a.tiles * a.splits));
   if constexpr (MANY) {
@@ -1007,13 +1008,8 @@ hipError_t attend_run(const AttendArgs& a, hipStream_t s) {
     else k_attend<T, D, NB, false><<<grid, kFewThreads, 0, s>>>(a);
   }
   hipError_t e = hipGetLastError();
-  // (k_attend adds up the scores of rows that one workgroup has whole)
-  if (e != hipSuccess || (a.splits == 1 && (!a.score || (!MANY && a.tiles == 1)))) return e;
-  const int each = a.splits <= kFewSplits ? kAtThreads / (D / 4) : 1;      // rows of a workgroup
-  const int row_groups = a.splits > 1 ? (int)(((int64_t)pairs * a.r_max + each - 1) / each) : 0;
-  const int blocks = kAtThreads / score_lanes(a.r_max, a.splits);          // blocks of a workgroup
-  const int score_groups = a.score ? pairs * ((a.max_nb + blocks - 1) / blocks) : 0;
-  k_attend_join<T, D><<<dim3((unsigned)row_groups + score_groups), kAtThreads, 0, s>>>(a, row_groups);
+  if (e != hipSuccess || p.row_groups + p.score_groups == 0) return e;
+  k_attend_join<T, D><<<dim3((unsigned)(p.row_groups + p.score_groups)), kAtThreads, 0, s>>>(a, (int)p.row_groups);
   return hipGetLastError();
 }
 
@@ -1022,18 +1018,18 @@ hipError_t attend_nb(const AttendArgs& a, const AttendPlan& p, hipStream_t s) {
   constexpr bool f32 = sizeof(T) == 4;
   if (p.many) {
     if constexpr (!f32)
-      if (p.two) return attend_run<T, D, 1, true, kManyWaves, true>(a, s);
+      if (p.two) return attend_run<T, D, 1, true, kManyWaves, true>(a, p, s);
     if constexpr (f32 || D == 128) {
-      if (p.waves == 2) return attend_run<T, D, many_tiles(D, f32), true, 2>(a, s);
-      if (p.waves == 4) return attend_run<T, D, many_tiles(D, f32), true, 4>(a, s);
+      if (p.waves == 2) return attend_run<T, D, many_tiles(D, f32), true, 2>(a, p, s);
+      if (p.waves == 4) return attend_run<T, D, many_tiles(D, f32), true, 4>(a, p, s);
     }
     if constexpr (many_tiles(D, f32) == 2)
-      if (p.nb == 1) return attend_run<T, D, 1, true>(a, s);
-    return attend_run<T, D, many_tiles(D, f32), true>(a, s);
+      if (p.nb == 1) return attend_run<T, D, 1, true>(a, p, s);
+    return attend_run<T, D, many_tiles(D, f32), true>(a, p, s);
   }
   if constexpr (few_tiles(D, f32) == 2)
-    if (p.nb == 2) return attend_run<T, D, 2, false>(a, s);
-  return attend_run<T, D, 1, false>(a, s);
+    if (p.nb == 2) return attend_run<T, D, 2, false>(a, p, s);
+  return attend_run<T, D, 1, false>(a, p, s);
 }
 
 }  // namespace
@@ -1114,6 +1110,15 @@ AttendPlan attend_plan(int n_seqs, int hk, int group, int d, int dtype, int max_
     p.splits_max = p.slots / hk - (n_seqs - 1);
     p.splits_max = p.splits_max < kMaxSplits ? p.splits_max : kMaxSplits;
   }
+  // (k_attend adds up the scores of rows that one workgroup has whole)
+  const bool join = p.splits > 1 || (score && (p.many || p.tiles > 1));
+  const int each = p.splits <= kFewSplits ? kAtThreads / (d / 4) : 1;         // rows of a workgroup
+  const int blocks = kAtThreads / score_lanes(p.r_max, p.splits);             // blocks of a workgroup
+  p.row_groups = p.splits > 1 ? (pairs * p.r_max + each - 1) / each : 0;
+  p.score_groups = join && score ? pairs * ((p.max_nb + blocks - 1) / blocks) : 0;
+  p.threads = (p.slots ? p.slots : wgs * p.splits) * kFewThreads;             // (k_attend_many: twice, in small grids alone)
+  const int64_t joins = (p.row_groups + p.score_groups) * kAtThreads;
+  p.threads = p.threads > joins ? p.threads : joins;
   const size_t parts = (size_t)p.splits_max * pairs;
   auto up256 = [](size_t v) { return (v + 255) & ~size_t(255); };
   size_t off = PI_WS_HEADER_BYTES;

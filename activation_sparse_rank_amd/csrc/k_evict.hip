@@ -337,6 +337,10 @@ __global__ __launch_bounds__(kEvThreads) void k_kv_evict(EvictArgs a) {
 
 }  // namespace
 
+int64_t kv_evict_threads(const EvictArgs& a) {
+  return (int64_t)a.n_seqs * a.hk * (a.max_blocks <= kRankMax ? (a.max_blocks + kWave - 1) / kWave * kWave : kEvThreads);
+}
+
 hipError_t launch_kv_evict(const EvictArgs& a, hipStream_t s) {
   const dim3 grid((unsigned)a.n_seqs * a.hk);
   const int v = (a.max_blocks + kEvThreads - 1) / kEvThreads;

@@ -230,6 +230,10 @@ hipError_t by_type(const CacheArgs& a, F f) {
 
 }  // namespace
 
+int64_t kv_cache_threads(const CacheArgs& a) {
+  return (int64_t)a.n_seqs * a.hk * 2 * touched_blocks(a.max_new) * kv_threads(a.d);
+}
+
 hipError_t launch_kv_append(const CacheArgs& a, hipStream_t s) {
   const int count = touched_blocks(a.max_new);
   const dim3 grid((unsigned)a.n_seqs * a.hk * 2 * count);

@@ -171,12 +171,20 @@ __global__ __launch_bounds__(kRopeThreads) void k_qk_rope(RopeArgs a, int group,
   }
 }
 
-template <typename T, int KIND>
-hipError_t rope_kind(const RopeArgs& a, hipStream_t s) {
-  constexpr int V = Vec<T>::N;
-  const int lanes = KIND == kRopePairs ? a.rot / 2 / V + (a.d - a.rot) / V : a.d / V;
-  int group = 1;                                      // a power of two, so that a head stays in a wave
-  while (group < lanes) group *= 2;
+int rope_kind(const RopeArgs& a) {
+  if (a.layout == PI_ROPE_INTERLEAVED) return kRopeInter;
+  return (a.rot / 2) % (a.dtype == PI_F16 ? Vec<f16>::N : Vec<float>::N) ? kRopeAny : kRopePairs;
+}
+
+struct RopeGrid {
+  int group, threads, hsplit;      // lanes of a head; of a workgroup; workgroups of a token
+};
+RopeGrid rope_grid(const RopeArgs& a) {
+  const int V = a.dtype == PI_F16 ? Vec<f16>::N : Vec<float>::N;
+  const int lanes = rope_kind(a) == kRopePairs ? a.rot / 2 / V + (a.d - a.rot) / V : a.d / V;
+  RopeGrid g;
+  g.group = 1;                                        // a power of two, so that a head stays in a wave
+  while (g.group < lanes) g.group *= 2;
   const int n_heads = a.in[0].n + a.in[1].n;
   // A token's heads in passes of one size.  Threads by what fills the card, at
   // least 256: 4096 tokens of 72 fp16 heads 31.9 us with 256 (three passes) and 46.7
@@ -184,26 +192,40 @@ hipError_t rope_kind(const RopeArgs& a, hipStream_t s) {
   // tokens: a pass to a workgroup of few threads.
   int most = 256;
   while (most < kRopeThreads && (int64_t)a.n_tok * most < kRopeFill) most *= 2;
-  while (most > 256 && (int64_t)a.n_tok * (((int64_t)n_heads * group + most - 1) / most) < kRopeMinGroups) most /= 2;
-  const int passes = (int)(((int64_t)n_heads * group + most - 1) / most);
-  const int threads = (int)(((int64_t)n_heads * group + passes - 1) / passes + kWave - 1) / kWave * kWave;
-  int hsplit = (kRopeMinGroups + a.n_tok - 1) / a.n_tok;
-  hsplit = hsplit < passes ? hsplit : passes;
-  const dim3 grid((unsigned)a.n_tok * hsplit);
+  while (most > 256 && (int64_t)a.n_tok * (((int64_t)n_heads * g.group + most - 1) / most) < kRopeMinGroups) most /= 2;
+  const int passes = (int)(((int64_t)n_heads * g.group + most - 1) / most);
+  g.threads = (int)(((int64_t)n_heads * g.group + passes - 1) / passes + kWave - 1) / kWave * kWave;
+  const int64_t hsplit = ((int64_t)kRopeMinGroups + a.n_tok - 1) / a.n_tok;
+  g.hsplit = (int)(hsplit < passes ? hsplit : passes);
+  return g;
+}
+
+template <typename T, int KIND>
+hipError_t rope_run(const RopeArgs& a, hipStream_t s) {
+  const RopeGrid g = rope_grid(a);
+  const dim3 grid((unsigned)a.n_tok * g.hsplit);
   if (a.w[0] || a.w[1])
-    k_qk_rope<T, KIND, true><<<grid, threads, 0, s>>>(a, group, hsplit);
+    k_qk_rope<T, KIND, true><<<grid, g.threads, 0, s>>>(a, g.group, g.hsplit);
   else
-    k_qk_rope<T, KIND, false><<<grid, threads, 0, s>>>(a, group, hsplit);
+    k_qk_rope<T, KIND, false><<<grid, g.threads, 0, s>>>(a, g.group, g.hsplit);
   return hipGetLastError();
 }
 
 template <typename T>
 hipError_t rope_type(const RopeArgs& a, hipStream_t s) {
-  if (a.layout == PI_ROPE_INTERLEAVED) return rope_kind<T, kRopeInter>(a, s);
-  return (a.rot / 2) % Vec<T>::N ? rope_kind<T, kRopeAny>(a, s) : rope_kind<T, kRopePairs>(a, s);
+  switch (rope_kind(a)) {
+    case kRopeInter: return rope_run<T, kRopeInter>(a, s);
+    case kRopePairs: return rope_run<T, kRopePairs>(a, s);
+    default: return rope_run<T, kRopeAny>(a, s);
+  }
 }
 
 }  // namespace
+
+int64_t qk_rope_threads(const RopeArgs& a) {
+  const RopeGrid g = rope_grid(a);
+  return (int64_t)a.n_tok * g.hsplit * g.threads;
+}
 
 hipError_t launch_qk_rope(const RopeArgs& a, hipStream_t s) {
   return a.dtype == PI_F16 ? rope_type<f16>(a, s) : rope_type<float>(a, s);

@@ -244,6 +244,9 @@ hipError_t launch_gather_read(const void* src, int n_rows, int row_bytes, const 
 
 // ---- The attention side (pi.h says what each computes) --------------------
 
+// A launch holds fewer than 2^32 threads.
+constexpr int64_t kMaxThreads = 0xffffffffll;
+
 // Rows [n_tok][n_heads][head_dim] of a call; strides in elements.
 struct HeadRows {
   void* p;
@@ -259,6 +262,7 @@ struct RopeArgs {
   HeadRows in[2], out[2];   // queries, keys
   const int32_t* pos;
 };
+int64_t qk_rope_threads(const RopeArgs& a);
 hipError_t launch_qk_rope(const RopeArgs& a, hipStream_t s);
 
 struct CacheArgs {
@@ -272,6 +276,7 @@ struct CacheArgs {
   int max_new, n_tok;
   HeadRows kv[2];           // rows in (append) or out (read)
 };
+int64_t kv_cache_threads(const CacheArgs& a);      // of an append or a read
 hipError_t launch_kv_append(const CacheArgs& a, hipStream_t s);
 hipError_t launch_kv_read(const CacheArgs& a, hipStream_t s);
 
@@ -288,6 +293,8 @@ struct AttendPlan {
   float share_even, share_safe; // blocks to a workgroup per block of all sequences: evenly, and always enough
   int r_max;                // rows of a (sequence, kv head): max_q * group
   int max_nb;               // blocks of max_len
+  int64_t row_groups, score_groups; // workgroups of the join (0: none)
+  int64_t threads;          // of the larger launch
   size_t part, ml, lse, count;  // offsets in the workspace (after its header)
   size_t total;             // bytes, the header among them
 };
@@ -325,6 +332,7 @@ struct EvictArgs {
   float* score_out;
   int32_t* lens_out;
 };
+int64_t kv_evict_threads(const EvictArgs& a);
 hipError_t launch_kv_evict(const EvictArgs& a, hipStream_t s);
 
 // Records a HIP error for pi_last_error(); returns PI_E_HIP (abi.hip).

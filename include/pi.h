@@ -347,6 +347,8 @@ pi_status pi_permute_rows(const void* src, int32_t rows, int32_t row_bytes, cons
  *    or more than its table row (or max_len) holds is INVALID, and a page
  *    number outside [0, n_pages) is a BAD PAGE.  Each call says what becomes
  *    of them; nothing is read or written out of range.
+ *  - PI_E_SHAPE also for sizes of which a launch could not hold the threads
+ *    (2^32 - 1), before the first launch of the call.
  *
  * The cache.  A block is PI_KV_BLOCK tokens of one kv head of one sequence
  * and is stored as one page of 2 * PI_KV_BLOCK * head_dim bytes, the keys' half, then
@@ -457,7 +459,7 @@ size_t pi_attend_workspace_bytes(const pi_kv_cache* cache, int32_t n_heads, int3
  *   q, out:    [n_tok][n_heads][head_dim]; out must not overlap q
  *   max_q:     host bound on the new rows of a sequence (1: decode)
  *   max_len:   host bound on lens, in [1, max_blocks * PI_KV_BLOCK]
- *   scale:     of the logits, e.g. 1 / sqrt(head_dim); finite
+ *   scale:     of the logits, e.g. 1 / sqrt(head_dim); finite, not negative
  *   add_score: nonzero adds to score[s][h][b] the weights that the call's
  *              rows of kv head h's query heads gave to the tokens of block b
  *   ws:        workspace, zero-filled when new (its header collects flags)
