@@ -40,6 +40,37 @@ bool overlap(const void* a, size_t na, const void* b, size_t nb) {
   return x < y + nb && y < x + na;
 }
 
+// Whether rows [n_tok][n][d] and [n_tok][m][d] share a byte (or may: rows of unlike
+// token strides, or of very many heads, whose spans meet).  Parts of one buffer lie
+// in each other's spans: first their places inside a token are compared, then
+// every head with every other.
+bool rows_meet(const void* p, int64_t ts, int64_t hs, int n, const void* r, int64_t rts, int64_t rhs, int m, int n_tok,
+               int d, int dtype) {
+  if (n == 1) hs = 0;
+  if (m == 1) rhs = 0;
+  if (!overlap(p, span(ts, hs, n, n_tok, d, dtype), r, span(rts, rhs, m, n_tok, d, dtype))) return false;
+  if (n_tok > 1 && ts != rts) return true;
+  const int64_t size = elem_bytes(dtype), row = n_tok > 1 ? ts * size : 0, w = d * size;
+  const int64_t gap = (int64_t)(reinterpret_cast<uintptr_t>(r) - reinterpret_cast<uintptr_t>(p));
+  const int64_t np = hs * (n - 1) * size + w, nr = rhs * (m - 1) * size + w;
+  if (row && np <= row && nr <= row) {
+    const int64_t at = ((gap % row) + row) % row;             // where r's heads begin inside p's token
+    if (at >= np && at + nr <= row) return false;
+  }
+  if ((int64_t)n * m > 1 << 16) return true;
+  for (int i = 0; i < n; ++i)
+    for (int j = 0; j < m; ++j) {
+      const int64_t x = gap + (j * rhs - i * hs) * size;      // between the heads' first tokens
+      int64_t k = row ? -x / row : 0;                         // tokens that bring them nearest, one more or less
+      k = k > n_tok - 2 ? n_tok - 2 : k < 2 - n_tok ? 2 - n_tok : k;
+      for (int64_t e = row ? -1 : 0; e <= (row ? 1 : 0); ++e) {
+        const int64_t y = x + (k + e) * row;
+        if (y < w && -y < w) return true;
+      }
+    }
+  return false;
+}
+
 pi_status check_cache(const pi_kv_cache* c) {
   if (!c) return PI_E_NULL;
   if (c->dtype != PI_F16 && c->dtype != PI_F32) return PI_E_DTYPE;
@@ -137,27 +168,17 @@ pi_status pi_qk_rope(const pi_rope* rope, const void* q, int64_t q_tok_stride, i
     if (st == PI_OK) st = check_rows(x.out, x.ots, x.ohs, x.n, n_tok, d, dtype);
     if (st != PI_OK) return st;
   }
-  // An output is its own input, or apart from both inputs (fused projections
-  // interleave q and k, so two strided views may lie in each other's span:
-  // rows of one token stride are compared inside a token).
-  auto rows_meet = [&](const void* p, int64_t ts, int64_t hs, int n, const void* r, int64_t rts, int64_t rhs, int m) {
-    if (!overlap(p, span(ts, hs, n, n_tok, d, dtype), r, span(rts, rhs, m, n_tok, d, dtype))) return false;
-    const int64_t row = ts * elem_bytes(dtype);
-    if (n_tok == 1 || ts != rts || hs * (n - 1) + d > ts || rhs * (m - 1) + d > ts) return true;
-    const int64_t gap = (int64_t)(reinterpret_cast<uintptr_t>(r) - reinterpret_cast<uintptr_t>(p));
-    const int64_t at = ((gap % row) + row) % row;             // where r's heads begin inside p's token
-    const int64_t np = (hs * (n - 1) + d) * elem_bytes(dtype), nr = (rhs * (m - 1) + d) * elem_bytes(dtype);
-    return at < np || at + nr > row;
-  };
+  // An output is its own input, or apart from both inputs.
   for (int o = 0; o < 2; ++o)
     for (int i = 0; i < 2; ++i) {
       const pi::HeadRows &x = a.out[o], &y = a.in[i];
       if (x.n == 0 || y.n == 0) continue;
       const bool same = o == i && x.p == y.p && x.hs == y.hs && (n_tok == 1 || x.ts == y.ts);
-      if (!same && rows_meet(x.p, x.ts, x.hs, x.n, y.p, y.ts, y.hs, y.n)) return PI_E_RANGE;
+      if (!same && rows_meet(x.p, x.ts, x.hs, x.n, y.p, y.ts, y.hs, y.n, n_tok, d, dtype)) return PI_E_RANGE;
     }
   if (a.out[0].n && a.out[1].n &&
-      rows_meet(a.out[0].p, a.out[0].ts, a.out[0].hs, a.out[0].n, a.out[1].p, a.out[1].ts, a.out[1].hs, a.out[1].n))
+      rows_meet(a.out[0].p, a.out[0].ts, a.out[0].hs, a.out[0].n, a.out[1].p, a.out[1].ts, a.out[1].hs, a.out[1].n, n_tok,
+                d, dtype))
     return PI_E_RANGE;
   a.d = d;
   a.rot = rope->rot;
@@ -193,6 +214,9 @@ pi_status pi_kv_read(const pi_kv_cache* cache, const int32_t* lens, const int32_
   const pi_status st = cache_args(cache, lens, q_start, max_new, k_out, k_tok_stride, k_head_stride, v_out,
                                   v_tok_stride, v_head_stride, n_tok, &a);
   if (st != PI_OK) return st;
+  if (rows_meet(k_out, k_tok_stride, k_head_stride, cache->n_kv_heads, v_out, v_tok_stride, v_head_stride,
+                cache->n_kv_heads, n_tok, cache->head_dim, cache->dtype))
+    return PI_E_RANGE;
   const hipError_t e = pi::launch_kv_read(a, static_cast<hipStream_t>(stream));
   return e == hipSuccess ? PI_OK : pi::hip_failed(e);
 }

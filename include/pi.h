@@ -432,8 +432,9 @@ pi_status pi_kv_append(const pi_kv_cache* cache, const void* k, int64_t k_tok_st
 
 /* Read back the values that the cache holds for the last rows of each
  * sequence (tokens lens - new .. lens), scale * (code - 128) in fp32, rounded
- * once.  Rows of an invalid sequence and values of a bad page are NaN.
- * Errors: as pi_kv_append.  */
+ * once.  Rows of an invalid sequence and values of a bad page are NaN.  k_out and
+ * v_out must not overlap.
+ * Errors: as pi_kv_append, and PI_E_RANGE (overlap).  */
 pi_status pi_kv_read(const pi_kv_cache* cache, const int32_t* lens, const int32_t* q_start, int32_t max_new,
                      void* k_out, int64_t k_tok_stride, int64_t k_head_stride,
                      void* v_out, int64_t v_tok_stride, int64_t v_head_stride, int32_t n_tok, void* stream);
