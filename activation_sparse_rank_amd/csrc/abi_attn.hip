@@ -242,8 +242,7 @@ pi_status pi_attend(const pi_kv_cache* cache, const void* q, int64_t q_tok_strid
   if ((st = check_rows(out, o_tok_stride, o_head_stride, n_heads, n_tok, d, dtype)) != PI_OK) return st;
   if (!al4(lens) || !al4(q_start)) return PI_E_ALIGN;
   if (!isfinite(scale) || scale < 0.0f) return PI_E_RANGE;
-  if (overlap(q, span(q_tok_stride, q_head_stride, n_heads, n_tok, d, dtype), out,
-              span(o_tok_stride, o_head_stride, n_heads, n_tok, d, dtype)))
+  if (rows_meet(q, q_tok_stride, q_head_stride, n_heads, out, o_tok_stride, o_head_stride, n_heads, n_tok, d, dtype))
     return PI_E_RANGE;
   if (!ws) return PI_E_WORKSPACE;
   if (!al16(ws)) return PI_E_ALIGN;

@@ -35,3 +35,20 @@ def test_read_into_parts_of_a_buffer(name):
     pi.kv_read(c.c, ln, want[0], want[1])
     pi.kv_read(c.c, ln, k, v)
     assert torch.equal(k, want[0]) and torch.equal(v, want[1]) and not torch.equal(k, v)
+
+
+@pytest.mark.parametrize("name", list(PARTS))
+def test_attend_between_parts_of_a_buffer(name):
+    lens, hk, d = (90, 40), 3, 64
+    c = _filled(2, hk, d, torch.float16, lens)
+    ln = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    shape, parts = PARTS[name](4, 2 * hk, d)
+    q, out = parts(torch.zeros(shape, dtype=torch.float16, device=DEV))
+    q.copy_(torch.randn(q.shape, device=DEV))
+    want = torch.zeros((4, 2 * hk, d), dtype=torch.float16, device=DEV)
+    q0 = q.clone()
+    pi.attend(c.c, q0, ln, want)
+    pi.attend(c.c, q, ln, out)
+    assert torch.equal(out, want) and torch.equal(q, q0)
+    with pytest.raises(pi.PiError):
+        pi.attend(c.c, q, ln, q)
