@@ -81,9 +81,12 @@ __global__ __launch_bounds__(kRopeThreads) void k_qk_rope(RopeArgs a, int group,
   for (int i = threadIdx.x; i < half; i += blockDim.x) {
     double t = (double)a.pos[tok] * a.freqs[i];
     t -= rint(t);
+    const float f = (float)t;
     float s, c;
-    sincospif(2.f * (float)t, &s, &c);
-    cs[i] = float2{a.scale * c, a.scale * s};
+    sincospif(2.f * f, &s, &c);
+    // What fp32 leaves of the angle (2^-26 of a turn at most: its square is nothing).
+    const float r = (float)((t - (double)f) * 6.283185307179586);
+    cs[i] = float2{a.scale * __builtin_fmaf(-s, r, c), a.scale * __builtin_fmaf(c, r, s)};
   }
   if constexpr (NORM) {
     for (int i = threadIdx.x; i < a.d; i += blockDim.x) {
