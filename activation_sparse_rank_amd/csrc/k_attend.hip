@@ -126,6 +126,9 @@ __device__ __forceinline__ float row_max(float v) {
 
 // 1 / a sum of weights; 0 where there are none.
 __device__ __forceinline__ float inverse(float sum) { return sum == 0.f ? 0.f : 1.f / sum; }
+// Of a whole row: where it sees tokens, a sum of 0 is that of logits that are all
+// -infinity, whose softmax is NaN.
+__device__ __forceinline__ bool no_softmax(float sum, int sees) { return sum == 0.f && sees > 0; }
 
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
 __device__ __forceinline__ float log2_hw(float x) { return __builtin_amdgcn_logf(x); }
@@ -616,6 +619,10 @@ __global__ __launch_bounds__(kFewThreads, 2) void k_attend(AttendArgs a) {
     const int64_t at = w.part_at(a, r);
     const bool whole = w.splits == 1;
     T* p = static_cast<T*>(a.out) + w.out_at(a, r) + e0;
+    if (whole && no_softmax(sum, w.sees(a, r))) {
+#pragma unroll
+      for (int k = 0; k < E; ++k) v[k] = quiet_nan();
+    }
 #pragma unroll
     for (int k = 0; k < E; k += 4) {
       const f32x4 y = {v[k], v[k + 1], v[k + 2], v[k + 3]};
@@ -776,9 +783,10 @@ __device__ __forceinline__ void many_rows(const AttendArgs& a, const Walk& w, L&
     const bool whole = a.splits == 1;
     const int64_t at = w.part_at(a, r);
     T* p = static_cast<T*>(a.out) + w.out_at(a, r) + 4 * g;
+    const bool none = whole && no_softmax(rows.l[nb], rows.sees[nb]);
 #pragma unroll
     for (int t = 0; t < DT; ++t) {
-      if (whole) store4(p + 16 * t, rows.o[nb][t]);
+      if (whole) store4(p + 16 * t, none ? f32x4{quiet_nan(), quiet_nan(), quiet_nan(), quiet_nan()} : rows.o[nb][t]);
       else *reinterpret_cast<f32x4*>(a.part + at * D + 16 * t + 4 * g) = rows.o[nb][t];
     }
     if ((!whole || SCORE) && g == 0) a.ml[at] = float2{rows.m[nb], rows.l[nb]};
@@ -885,6 +893,7 @@ __global__ __launch_bounds__(kAtThreads) void k_attend_join(AttendArgs a, int ro
       }
       const int h = pair % a.hk;
       T* p = static_cast<T*>(a.out) + (int64_t)(q.q0 + r / a.group) * a.o_ts + (int64_t)(h * a.group + r % a.group) * a.o_hs;
+      if (no_softmax(sum, q.len - q.n + 1 + r / a.group)) o = f32x4{quiet_nan(), quiet_nan(), quiet_nan(), quiet_nan()};
       store4(p + e, o);
       return;
     }
@@ -909,7 +918,8 @@ __global__ __launch_bounds__(kAtThreads) void k_attend_join(AttendArgs a, int ro
 #pragma unroll
     for (int y = 32; y >= 1; y >>= 1) top = fmaxf(top, __shfl_xor(top, y, kWave));
     float f = exp2_hw(v.x - top) * v.y;
-    f *= inverse(wave_sum(f));
+    const float sum = wave_sum(f);
+    f *= inverse(sum);
     f32x4 o = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int k = 0; k < N; ++k) {
@@ -922,6 +932,7 @@ __global__ __launch_bounds__(kAtThreads) void k_attend_join(AttendArgs a, int ro
     if (part) return;
 #pragma unroll
     for (int i = 1; i < G; ++i) o += acc[i][e / 4];
+    if (no_softmax(sum, q.len - q.n + 1 + r / a.group)) o = f32x4{quiet_nan(), quiet_nan(), quiet_nan(), quiet_nan()};
     const int h = pair % a.hk;
     T* p = static_cast<T*>(a.out) + (int64_t)(q.q0 + r / a.group) * a.o_ts + (int64_t)(h * a.group + r % a.group) * a.o_hs + e;
     store4(p, o);
