@@ -193,7 +193,6 @@ def attend(cache: KVCache, q, lens, out, q_start=None, max_q=None, max_len=None,
     table holds); ``scale``: 1 / sqrt(head_dim) by default; ``add_score``: add the
     weights of each block to cache.score.  ``ws`` from alloc_attend_workspace
     with the same bounds (one is allocated where it is None)."""
-    d, dt, dev = cache.head_dim, cache.dtype, cache._dev
     if max_len is None:
         max_len = cache.max_blocks * L.PI_KV_BLOCK
     if ws is None:

@@ -697,7 +697,7 @@ __device__ __forceinline__ void many_rows(const AttendArgs& a, const Walk& w, L&
 #pragma unroll
       for (int k = 0; k < U; ++k) {
         const int u = wave_id() * U + k;
-        const int64_t page = __builtin_amdgcn_readlane(x.page, i + u / kUnits);
+        const int64_t page = __builtin_amdgcn_readlane(x.page, (i + u / kUnits) % kWave);
         next[k] = ld16(a.pages + page * (2 * kBlk * D) + u % kUnits * 1024 + lane * 16);
       }
     };
