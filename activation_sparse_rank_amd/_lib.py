@@ -15,8 +15,8 @@ PI_OK, PI_E_NULL, PI_E_SHAPE, PI_E_DTYPE, PI_E_ALIGN, PI_E_RANGE, PI_E_WORKSPACE
 PI_F32, PI_F16, PI_Q4_0 = 0, 1, 2
 PI_RELU, PI_REGLU, PI_RELU2 = 0, 1, 2
 PI_ROPE_HALF, PI_ROPE_INTERLEAVED = 0, 1
-PI_KV_BLOCK = 32              # tokens of a cache block (pi.h)
-PI_KV_EVICT_IN_PLACE = 16384  # most blocks of a table row that pi_kv_evict works on in place (pi.h)
+PI_KV_BLOCK = 32              # tokens of a cache block (pi_attn.h)
+PI_KV_EVICT_IN_PLACE = 16384  # most blocks of a table row that pi_kv_evict works on in place (pi_attn.h)
 
 STATUS_NAMES = {
     PI_OK: "PI_OK", PI_E_NULL: "PI_E_NULL", PI_E_SHAPE: "PI_E_SHAPE", PI_E_DTYPE: "PI_E_DTYPE",
@@ -26,8 +26,9 @@ STATUS_NAMES = {
 # Every symbol include/pi.h declares.
 EXPORTS = ("pi_workspace_bytes", "pi_clear_flags", "pi_read_flags", "pi_read_down_rows", "pi_read_up_rows", "pi_predict", "pi_compact",
            "pi_sparse_ffn", "pi_layer", "pi_layer_noalloc", "pi_q4_0_repack", "pi_count_active", "pi_hot_order",
-           "pi_rank_order", "pi_permute_rows", "pi_stream_read", "pi_gather_read", "pi_status_str", "pi_last_error",
-           "pi_qk_rope", "pi_kv_append", "pi_kv_read", "pi_attend_workspace_bytes", "pi_attend", "pi_kv_evict")
+           "pi_rank_order", "pi_permute_rows", "pi_stream_read", "pi_gather_read", "pi_status_str", "pi_last_error")
+# And every symbol include/pi_attn.h declares.
+ATTN_EXPORTS = ("pi_qk_rope", "pi_kv_append", "pi_kv_read", "pi_attend_workspace_bytes", "pi_attend", "pi_kv_evict")
 
 PI_SEGMENT_ROWS = 32   # neurons per segment of pi_layer's fused kernel (pi.h)
 PI_STREAM_BLOCKS = 2048  # entries of pi_stream_read's output (pi.h)

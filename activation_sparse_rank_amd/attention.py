@@ -5,7 +5,7 @@ accumulated attention weight (``kv_evict``).
 
 As in ``api``, each function checks what the C ABI cannot see (devices,
 types, shapes, strides) and forwards pointers and the current HIP stream;
-include/pi.h says what each call computes.  The checks are native
+include/pi_attn.h says what each call computes.  The checks are native
 (csrc/bind_attn.cpp): these calls run for a few microseconds each, once or more per
 layer and token.  Token rows are
 [n_tok, n_heads, head_dim] tensors whose last dimension is contiguous, so

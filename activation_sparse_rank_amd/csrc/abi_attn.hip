@@ -1,9 +1,9 @@
-// C ABI of the attention side (declared in include/pi.h): host checks and
+// C ABI of the attention side (declared in include/pi_attn.h): host checks and
 // launches.  Every check comes before the first launch.
 #include <math.h>
 
+#include "attn_internal.h"
 #include "pi.h"
-#include "pi_internal.h"
 
 namespace {
 

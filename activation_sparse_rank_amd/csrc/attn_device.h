@@ -2,7 +2,7 @@
 // as floats, and the checks of values that live in device memory.
 #pragma once
 
-#include "pi_internal.h"
+#include "attn_internal.h"
 
 namespace pi {
 

@@ -1,5 +1,5 @@
 // Python entry points of the attention side: checks of tensors and the C
-// ABI's calls (include/pi.h), for attention.py.
+// ABI's calls (include/pi_attn.h), for attention.py.
 //
 // A decode step's calls take 3 to 10 microseconds on the GPU.  The same checks
 // in Python, with the arguments' way through ctypes, took as long again, so the
