@@ -26,14 +26,14 @@
 // CUs (few rows of unlike sequences by their lengths, Shares); partial means are
 // joined in a fixed order (in LDS, then in k_attend_join).
 //
-// Measured (streaming read 6.45 TB/s, fp16 product 1150 TFLOP/s on the same
-// card): one token of 64 heads over 131072 tokens of 8 kv heads, D = 128, 48.0 us with
-// the join (269 MB, 5.6 TB/s); 32 sequences of 16384 tokens and less with
-// scores 158 us (863 MB, 5.5 TB/s); fp32, 56 kv heads of their own, 34.0 us (180
-// MB, 5.3 TB/s); 512 tokens of 128 heads over 8200 tokens, D = 64, 159 us (133
-// GFLOP, 840 TFLOP/s): there the instructions around the products bind, 230 k
-// cycles a SIMD beside the products' 143 k, of 350 k; 4096 tokens of 64 heads, 8 of
-// kv, D = 128, whole, 294 us (275 GFLOP, 935 TFLOP/s).
+// Measured (streaming read 6.45 TB/s, fp16 product 1160 TFLOP/s on the same
+// card): one token of 64 heads over 131072 tokens of 8 kv heads, D = 128, 48.5 us with
+// the join (269 MB, 5.5 TB/s); 32 sequences of 16384 tokens and less with
+// scores 156 us (863 MB, 5.5 TB/s); fp32, 56 kv heads of their own, 34.2 us (180
+// MB, 5.3 TB/s); 512 tokens of 128 heads over 8200 tokens, D = 64, 162 us (133
+// GFLOP, 820 TFLOP/s): there the instructions around the products bind, 232 k
+// cycles a SIMD beside the products' 144 k, of 367 k; 4096 tokens of 64 heads, 8 of
+// kv, D = 128, whole, 312 us (275 GFLOP, 880 TFLOP/s).
 #include "attn_device.h"
 
 namespace pi {

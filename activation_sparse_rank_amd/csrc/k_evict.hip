@@ -13,7 +13,8 @@
 //    that the threshold falls into, seldom many, are ranked among themselves by
 //    counting; where they are many, the bin is cut into 2048 again.
 // Ballots then give every block its place.
-// Measured: 130 blocks 4.2 us a call, 32 x 8 rows of 4099 blocks 10.3 us.
+// Measured: 130 blocks 4.2 us a call, 32 x 8 rows of 4099 blocks 10.4 us (waves wait 60% of
+// their time), 8 rows of 9003 blocks 16, of 20003 43 us.
 #include "attn_device.h"
 
 namespace pi {
